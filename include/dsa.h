@@ -77,8 +77,11 @@ typedef enum {
   DSA_OP_TOPK = 1,
   DSA_OP_SPARSE_ATTN = 2,
   DSA_OP_FORWARD = 3,
-  DSA_OP_INDEXER_KL = 4
+  DSA_OP_INDEXER_KL = 4,
+  DSA_OP_DENSE_ATTN = 5
 } dsa_op;
+
+typedef enum { DSA_F32 = 0, DSA_BF16 = 1 } dsa_dtype;
 
 typedef struct {
   int32_t batch;          /* B                                              */
@@ -333,6 +336,155 @@ dsa_status dsa_indexer_kl(const dsa_shape* shape, const uint8_t* q_fp8,
                           float* loss, float* dw, float* dq, float* dk,
                           void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Dense MQA attention of a few new tokens over the whole latent cache (page
+ * "DeepSeek architecture", section 1.1, MLA with absorbed projections; the
+ * dense warm-up stage of page "DeepseekV3.2 拆解" attends this way, and so
+ * does a decode step whose context is not longer than topk).
+ *   q       [B, n_q, H, D_qk] bf16
+ *   kv      [B, n_kv, D_qk] bf16 latent rows, or a page pool
+ *   out     [B, n_q, H, D_v] fp32 or bf16 (out_dtype)
+ *   lse     [B, n_q, H] fp32 natural-log sum of exp of the logits, or NULL
+ *   p = softmax(softmax_scale * q . kv[s]) over every key s the row sees
+ *   (s <= position and s < kv_len), out = p kv[:, :D_v].
+ *   A row that sees no key gets out = 0 and lse = -inf. Cache rows past
+ *   kv_len are never used, whatever they hold. p is rounded to bf16 for the
+ *   product with V and O is divided by the sum of the rounded p; every sum,
+ *   maximum and the lse are fp32.
+ *   The caches' keys are cut into equal shares per SM pair on the device, so
+ *   lengths may be ragged; the results are the same bits on every call.
+ *   Supported: qk_dim = 576, v_dim = 512, heads 1..128, softmax_scale > 0,
+ *   B * n_q <= 65536; idx_heads, idx_dim and topk are not looked at.
+ *   Workspace: dsa_workspace_size(shape, DSA_OP_DENSE_ATTN) bytes, 256-byte
+ *   aligned, the same for every length. Calls that may overlap on the GPU
+ *   (two streams, two graphs) need a workspace each.
+ */
+dsa_status dsa_dense_attn(const dsa_shape* shape, const uint16_t* q, const uint16_t* kv,
+                          const int32_t* q_pos0, const int32_t* kv_len, void* out,
+                          int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream);
+dsa_status dsa_dense_attn_ex(const dsa_shape* shape, const dsa_layout* layout, const uint16_t* q,
+                             const uint16_t* kv, const int32_t* q_pos0, const int32_t* kv_len,
+                             void* out, int32_t out_dtype, float* lse, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/*
+ * Rotary positions (page "DeepSeek architecture", section 1.1: the decoupled
+ * RoPE dims of q and of the latent row; the indexer's q and k carry positions
+ * the same way). Dims [rot_begin, rot_begin + rot_dim) of a head turn in
+ * rot_dim / 2 pairs; pair i turns by position * freq[i] radians and is scaled
+ * by amplitude. Host struct, filled by dsa_rope_init or by the caller.
+ */
+typedef enum { DSA_ROPE_HALF = 0, DSA_ROPE_INTERLEAVED = 1 } dsa_rope_layout;
+typedef enum { DSA_ROPE_PLAIN = 0, DSA_ROPE_LINEAR = 1, DSA_ROPE_YARN = 2 } dsa_rope_scaling;
+
+typedef struct {
+  int32_t rot_dim;     /* even, 2..256                                        */
+  int32_t rot_begin;   /* first rotated dim                                   */
+  int32_t layout;      /* dsa_rope_layout: pairs (i, i + rot_dim / 2) or
+                          (2i, 2i + 1)                                        */
+  float amplitude;     /* factor of cos and sin (1: a pure rotation)          */
+  double freq[128];    /* radians per position of pair i < rot_dim / 2        */
+} dsa_rope_spec;
+
+/*
+ * Frequencies f_i = base^(-2i / rot_dim), scaled for contexts `factor` times
+ * longer than orig_context:
+ *   DSA_ROPE_PLAIN   f_i
+ *   DSA_ROPE_LINEAR  f_i / factor
+ *   DSA_ROPE_YARN    (1 - g) f_i / factor + g f_i, with
+ *                    g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
+ *                    and r = orig_context f_i / (2 pi), the turns that pair i
+ *                    makes over the original context.
+ * factor, orig_context and the betas are looked at only where they are used.
+ * Host-only.
+ */
+dsa_status dsa_rope_init(dsa_rope_spec* spec, int32_t rot_dim, int32_t rot_begin, int32_t layout,
+                         double base, int32_t scaling, double factor, int32_t orig_context,
+                         double beta_fast, double beta_slow, float amplitude);
+
+/* The tensor of a dsa_rope call: [B, n_q, heads, dim] with any strides (in
+ * elements) of the first three; dim is contiguous. */
+typedef struct {
+  int32_t batch, n_q, heads, dim;
+  int32_t dtype;          /* dsa_dtype of x and out */
+  int64_t x_stride[3];    /* of batch, n_q, heads   */
+  int64_t out_stride[3];
+} dsa_rope_view;
+
+/*
+ * out = x with its rotated dims turned by each token's position (q_pos0[b] +
+ * i, or row_pos[b, i] where row_pos is given; both NULL: i). backward != 0
+ * applies the transpose (the turn by minus the angle, the same amplitude):
+ * the gradient of x from that of out.
+ *   out == x (and equal strides) rotates in place and touches only the rotated dims;
+ *   otherwise the other dims are copied, and out must not overlap x.
+ *   A token at a negative position is padding: its rows of out are left as
+ *   they were.
+ *   Arithmetic in fp32 with angles reduced in fp64; one rounding to dtype.
+ */
+dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* view, const void* x, void* out,
+                    const int32_t* q_pos0, const int32_t* row_pos, int32_t backward, void* stream);
+
+/*
+ * Layer norm over rows of dim values (the indexer's key norm):
+ *   y = (x - mean) * rstd * weight + bias, rstd = 1 / sqrt(var + eps),
+ *   var the mean of (x - mean)^2.
+ *   x, y    [rows, dim] fp32 or bf16 each, row strides in elements
+ *   weight, bias [dim] fp32, NULL = 1 and 0
+ *   mean, rstd [rows] fp32, each may be NULL (the gradient needs both)
+ *   1 <= dim <= 16384; y may be x (same dtype and stride), else they must not
+ *   overlap; rows = 0 launches nothing. Statistics in fp32 from two passes.
+ */
+dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype,
+                         int64_t x_stride, const float* weight, const float* bias, float eps,
+                         void* y, int32_t y_dtype, int64_t y_stride, float* mean, float* rstd,
+                         void* stream);
+
+/*
+ * Its gradient. xh = (x - mean) rstd, g = dy * weight:
+ *   dx = rstd (g - mean(g) - xh mean(g xh)), dweight = sum over rows of
+ *   dy xh, dbias = sum over rows of dy (zeros for rows = 0).
+ *   dy, x, dx [rows, dim] fp32 or bf16 each; dx may be dy or x (same dtype
+ *   and stride). weight NULL = 1. dweight and dbias [dim] fp32 may be NULL.
+ *   The row sums are fp32, in a fixed order: the same bits on every call.
+ *   Workspace: dsa_layernorm_bwd_workspace bytes, 16-byte aligned (none is
+ *   needed when dweight and dbias are both NULL).
+ */
+dsa_status dsa_layernorm_bwd_workspace(int64_t rows, int32_t dim, size_t* bytes);
+dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t dy_dtype,
+                             int64_t dy_stride, const void* x, int32_t x_dtype, int64_t x_stride,
+                             const float* weight, const float* mean, const float* rstd, void* dx,
+                             int32_t dx_dtype, int64_t dx_stride, float* dweight, float* dbias,
+                             void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * New tokens into the caches that the calls above read, in one launch (page
+ * "DeepSeek-V3 MoE blog", section 4.1: the paged cache's append). Token i of
+ * sequence b, i < n_new[b], goes to logical key s = q_pos0[b] + i:
+ *   kv[s]                = c with its dims rotated by kv_rope at s;
+ *   k_fp8[s], k_scale[s] = row encoding (as dsa_quantize_e4m3) of
+ *                          rope(layernorm(k)) by idx_rope at s.
+ *   k       [B, n_q, d^I] bf16     c       [B, n_q, D_qk] bf16
+ *   ln_weight, ln_bias [d^I] fp32, NULL = 1 and 0
+ *   q_pos0  [B] int32 or NULL (0)  n_new   [B] int32 or NULL (n_q): tokens
+ *           past n_new[b] are padding and write nothing
+ *   k_fp8, k_scale, kv: the caches (layout as for dsa_forward; NULL =
+ *           contiguous [B, n_kv, ...]). n_kv of the shape is their capacity.
+ *   The key stays in fp32 from its load to its codes. A token whose position
+ *   is outside [0, n_kv), or whose page is outside the pool, writes nothing
+ *   and the next dsa_check() returns DSA_ERR_INVALID_ARG. Two sequences must
+ *   not append to one page; layout->row_pos must be NULL (a sequence's new
+ *   tokens are consecutive). k and c must not overlap the caches.
+ *   Supported: idx_dim in {32, 128}, qk_dim in {64, 576}; both specs inside
+ *   their rows (rot_begin + rot_dim <= idx_dim, qk_dim).
+ */
+dsa_status dsa_cache_append(const dsa_shape* shape, const dsa_layout* layout, const uint16_t* k,
+                            const float* ln_weight, const float* ln_bias, float eps,
+                            const dsa_rope_spec* idx_rope, const uint16_t* c,
+                            const dsa_rope_spec* kv_rope, const int32_t* q_pos0,
+                            const int32_t* n_new, uint8_t* k_fp8, float* k_scale, uint16_t* kv,
+                            void* stream);
+
 /* Rows per indexer/top-k step that dsa_forward uses for this shape. With
  * the fused plan it is n_q (one dsa_indexer_topk launch over all rows, no
  * score storage). Otherwise the scores of `rows` query rows (rows * n_kv
@@ -360,8 +512,8 @@ dsa_status dsa_workspace_size(const dsa_shape* shape, int32_t op,
 
 /* Synchronises `stream`, then returns DSA_ERR_CUDA for a pending CUDA error,
  * DSA_ERR_TIMEOUT if a kernel's bounded wait ran out since the last check,
- * DSA_ERR_INVALID_ARG if a kernel met a block-table page outside its pool
- * (the error word is cleared), else DSA_OK. */
+ * DSA_ERR_INVALID_ARG if a kernel met a block-table page outside its pool or
+ * an append past its cache (the error word is cleared), else DSA_OK. */
 dsa_status dsa_check(void* stream);
 
 /* Static description of a status code. */

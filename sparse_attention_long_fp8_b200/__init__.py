@@ -35,6 +35,16 @@ DSA_OP_TOPK = 1
 DSA_OP_SPARSE_ATTN = 2
 DSA_OP_FORWARD = 3
 DSA_OP_INDEXER_KL = 4
+DSA_OP_DENSE_ATTN = 5
+
+DSA_F32 = 0
+DSA_BF16 = 1
+
+DSA_ROPE_HALF = 0
+DSA_ROPE_INTERLEAVED = 1
+DSA_ROPE_PLAIN = 0
+DSA_ROPE_LINEAR = 1
+DSA_ROPE_YARN = 2
 
 
 class DsaError(RuntimeError):
@@ -56,6 +66,20 @@ class DsaLayout(ctypes.Structure):
     _fields_ = [("row_pos", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
                 ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("pool_rows", ctypes.c_int64)]
+
+
+class DsaRopeSpec(ctypes.Structure):
+    """dsa_rope_spec: which dims of a head turn, and how fast (see rope_spec)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("rot_begin", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("freq", ctypes.c_double * 128)]
+
+
+class DsaRopeView(ctypes.Structure):
+    """dsa_rope_view: sizes, dtype and element strides of a dsa_rope call."""
+    _fields_ = [("batch", ctypes.c_int32), ("n_q", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("x_stride", ctypes.c_int64 * 3), ("out_stride", ctypes.c_int64 * 3)]
 
 
 def make_layout(row_pos=None, block_table=None, page_size=0, pool_rows=0):
@@ -113,6 +137,17 @@ def load_library(path: str | None = None):
     lib.dsa_topk_ex.argtypes = [SP, LP, P, I32, I32, P, P, P, P, SZ, P]
     lib.dsa_sparse_attn_ex.argtypes = [SP, LP, P, P, P, P, I32, P, P, SZ, P]
     lib.dsa_forward_ex.argtypes = [SP, LP, P, P, P, P, P, P, P, P, P, P, P, I32, P, P, SZ, P]
+    I64, F32, F64 = ctypes.c_int64, ctypes.c_float, ctypes.c_double
+    RP = ctypes.POINTER(DsaRopeSpec)
+    lib.dsa_dense_attn.argtypes = [SP, P, P, P, P, P, I32, P, P, SZ, P]
+    lib.dsa_dense_attn_ex.argtypes = [SP, LP, P, P, P, P, P, I32, P, P, SZ, P]
+    lib.dsa_rope_init.argtypes = [RP, I32, I32, I32, F64, I32, F64, I32, F64, F64, F32]
+    lib.dsa_rope.argtypes = [RP, ctypes.POINTER(DsaRopeView), P, P, P, P, I32, P]
+    lib.dsa_layernorm.argtypes = [I64, I32, P, I32, I64, P, P, F32, P, I32, I64, P, P, P]
+    lib.dsa_layernorm_bwd_workspace.argtypes = [I64, I32, ctypes.POINTER(SZ)]
+    lib.dsa_layernorm_bwd.argtypes = [I64, I32, P, I32, I64, P, I32, I64, P, P, P, P, I32, I64, P,
+                                      P, P, SZ, P]
+    lib.dsa_cache_append.argtypes = [SP, LP, P, P, P, F32, RP, P, RP, P, P, P, P, P, P]
     lib.dsa_status_string.argtypes = [ctypes.c_int]
     lib.dsa_status_string.restype = ctypes.c_char_p
     lib.dsa_last_error.restype = ctypes.c_char_p
@@ -121,7 +156,9 @@ def load_library(path: str | None = None):
                "dsa_workspace_size", "dsa_check", "dsa_forward_chunk_rows",
                "dsa_sparse_attn_noalloc", "dsa_forward_plan", "dsa_indexer_scores_ex",
                "dsa_indexer_topk_ex", "dsa_topk_ex", "dsa_sparse_attn_ex", "dsa_forward_ex",
-               "dsa_indexer_kl"):
+               "dsa_indexer_kl", "dsa_dense_attn", "dsa_dense_attn_ex", "dsa_rope_init", "dsa_rope",
+               "dsa_layernorm", "dsa_layernorm_bwd_workspace", "dsa_layernorm_bwd",
+               "dsa_cache_append"):
         getattr(lib, fn).restype = ctypes.c_int
     if path == LIB_PATH:
         _lib = lib
@@ -316,6 +353,201 @@ def indexer_kl(inp: dict, cfg: DsaConfig, stream=None):
                    inp["q_pos0"], inp["kv_len"], inp["q"], inp["kv"], loss, dw, dq, dk, ws, n,
                    stream)
     return {"loss": loss, "dw": dw, "dq": dq, "dk": dk}
+
+
+# ------------------------------------------------------------------ next to the path
+
+def _on_device(t, stream, what="tensor"):
+    """(context manager, raw stream) of a launch on t's device: that device is
+    made current for the call, and None means its current stream."""
+    import contextlib
+
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    idx = t.device.index
+    here = torch.cuda.current_device() == idx
+    if stream is None:
+        stream = torch.cuda.current_stream(idx).cuda_stream
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    return (contextlib.nullcontext() if here else torch.cuda.device(idx)), stream
+
+
+def _arg(t, dtypes, shape, device, what):
+    """Raw pointer of a contiguous tensor of the given dtypes and shape on
+    `device` (None -> NULL)."""
+    if t is None:
+        return None
+    if t.device != device:
+        raise ValueError(f"{what} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def _dtype_code(t, what):
+    import torch
+    if t.dtype == torch.bfloat16:
+        return DSA_BF16
+    if t.dtype == torch.float32:
+        return DSA_F32
+    raise ValueError(f"{what} has dtype {t.dtype}, expected bfloat16 or float32")
+
+
+def rope_spec(rot_dim, rot_begin=0, layout=DSA_ROPE_HALF, base=10000.0, scaling=DSA_ROPE_PLAIN,
+              factor=1.0, orig_context=0, beta_fast=32.0, beta_slow=1.0, amplitude=1.0):
+    """A DsaRopeSpec with the frequencies of dsa_rope_init (plain, linear or
+    YaRN scaling). Its ``freq`` may be overwritten (radians per position)."""
+    spec = DsaRopeSpec()
+    _raise(load_library().dsa_rope_init(ctypes.byref(spec), int(rot_dim), int(rot_begin),
+                                        int(layout), float(base), int(scaling), float(factor),
+                                        int(orig_context), float(beta_fast), float(beta_slow),
+                                        float(amplitude)))
+    return spec
+
+
+def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=None):
+    """Rotary positions: out = x [B, T, H, D] (bf16 or fp32, any strides, D
+    contiguous) with the spec's dims turned by each token's position; out may
+    be x. backward applies the transpose."""
+    import torch
+    if x.dim() != 4 or x.shape != out.shape:
+        raise ValueError("x and out must be [B, T, H, D] of the same shape")
+    if x.dtype != out.dtype or x.device != out.device:
+        raise ValueError("x and out must have the same dtype and device")
+    B, T, H, D = x.shape
+    xs, os_ = x.stride(), out.stride()
+    if D > 1 and (xs[3] != 1 or os_[3] != 1):
+        raise ValueError("the last dim of x and out must be contiguous")
+    code = _dtype_code(x, "x")
+    p0 = _arg(q_pos0, (torch.int32,), (B,), x.device, "q_pos0")
+    rp = _arg(row_pos, (torch.int32,), (B, T), x.device, "row_pos")
+    ctx, st = _on_device(x, stream, "x")
+    if x.numel() == 0:
+        return
+    view = DsaRopeView(B, T, H, D, code, xs[:3], os_[:3])
+    with ctx:
+        _raise(load_library().dsa_rope(ctypes.byref(spec), ctypes.byref(view), x.data_ptr(),
+                                       out.data_ptr(), p0, rp, 1 if backward else 0, st))
+
+
+def _rows(t, what):
+    """(rows, dim, row stride) of a tensor [..., dim] whose rows are evenly
+    spaced: contiguous, or a 2-D tensor with any row stride."""
+    if t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1):
+        return t.shape[0], t.shape[1], t.stride(0)
+    if t.dim() < 1 or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous, or 2-D with contiguous rows")
+    dim = t.shape[-1]
+    return (t.numel() // dim if dim else 0), dim, dim
+
+
+def dsa_layernorm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
+    """Layer norm over the last dim of x into y (bf16 or fp32 each); weight and
+    bias fp32 [dim] or None; mean and rstd fp32 [rows] receive the statistics."""
+    import torch
+    rows, dim, xs = _rows(x, "x")
+    f32, dev = (torch.float32,), x.device
+    if x.shape != y.shape or y.device != dev:
+        raise ValueError("y must have x's shape and device")
+    _, _, ys = _rows(y, "y")
+    xc, yc = _dtype_code(x, "x"), _dtype_code(y, "y")
+    w, b = _arg(weight, f32, (dim,), dev, "weight"), _arg(bias, f32, (dim,), dev, "bias")
+    stats = [None if t is None else _arg(t, f32, t.shape if t.numel() == rows else (rows,), dev, n)
+             for t, n in ((mean, "mean"), (rstd, "rstd"))]
+    ctx, st = _on_device(x, stream, "x")
+    if rows == 0:
+        return
+    with ctx:
+        _raise(load_library().dsa_layernorm(rows, dim, x.data_ptr(), xc, xs, w, b, float(eps),
+                                            y.data_ptr(), yc, ys, stats[0], stats[1], st))
+
+
+def layernorm_bwd_workspace(rows: int, dim: int) -> int:
+    n = ctypes.c_size_t(0)
+    _raise(load_library().dsa_layernorm_bwd_workspace(int(rows), int(dim), ctypes.byref(n)))
+    return n.value
+
+
+def dsa_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, ws=None,
+                      ws_bytes=0, stream=None):
+    """Gradient of dsa_layernorm: dx (bf16 or fp32), and dweight, dbias (fp32
+    [dim], may be None). ws holds layernorm_bwd_workspace(rows, dim) bytes."""
+    import torch
+    rows, dim, xs = _rows(x, "x")
+    f32, dev = (torch.float32,), x.device
+    for t, n in ((dy, "dy"), (dx, "dx")):
+        if t.shape != x.shape or t.device != dev:
+            raise ValueError(f"{n} must have x's shape and device")
+    _, _, dys = _rows(dy, "dy")
+    _, _, dxs = _rows(dx, "dx")
+    codes = _dtype_code(dy, "dy"), _dtype_code(x, "x"), _dtype_code(dx, "dx")
+    w = _arg(weight, f32, (dim,), dev, "weight")
+    stats = [_arg(t, f32, t.shape if t.numel() == rows else (rows,), dev, n)
+             for t, n in ((mean, "mean"), (rstd, "rstd"))]
+    dw, db = _arg(dweight, f32, (dim,), dev, "dweight"), _arg(dbias, f32, (dim,), dev, "dbias")
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    ctx, st = _on_device(x, stream, "x")
+    with ctx:
+        # an empty tensor has no address; with no rows nothing is read through it
+        some = (lambda t: t.data_ptr() or 256) if rows == 0 else (lambda t: t.data_ptr())
+        _raise(load_library().dsa_layernorm_bwd(
+            rows, dim, some(dy), codes[0], dys, some(x), codes[1], xs, w,
+            stats[0] or (256 if rows == 0 else None), stats[1] or (256 if rows == 0 else None),
+            some(dx), codes[2], dxs, dw, db, _ptr(ws, None, "ws"), int(ws_bytes), st))
+
+
+def dsa_cache_append(shape, k, ln_weight, ln_bias, eps, idx_rope, c, kv_rope, q_pos0, n_new,
+                     k_fp8, k_scale, kv, stream=None, layout=None):
+    """New tokens into the caches: indexer keys k [B, T, d^I] bf16 by layer
+    norm, rotation and row encoding into k_fp8 / k_scale, latent rows c
+    [B, T, D_qk] bf16 by rotation into kv, at positions q_pos0[b] + i for
+    i < n_new[b]."""
+    import torch
+    B, T, dev = shape.batch, shape.n_q, k.device
+    f32, i32, bf16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+    pool = layout.pool_rows if layout is not None and layout.block_table else B * shape.n_kv
+    for t, per, n in ((k_fp8, shape.idx_dim, "k_fp8"), (k_scale, 1, "k_scale"), (kv, shape.qk_dim, "kv")):
+        if t.numel() != pool * per:
+            raise ValueError(f"{n} has {t.numel()} elements, the cache has {pool} rows of {per}")
+    args = (_arg(k, bf16, (B, T, shape.idx_dim), dev, "k"),
+            _arg(ln_weight, f32, (shape.idx_dim,), dev, "ln_weight"),
+            _arg(ln_bias, f32, (shape.idx_dim,), dev, "ln_bias"), float(eps), ctypes.byref(idx_rope),
+            _arg(c, bf16, (B, T, shape.qk_dim), dev, "c"), ctypes.byref(kv_rope),
+            _arg(q_pos0, i32, (B,), dev, "q_pos0"), _arg(n_new, i32, (B,), dev, "n_new"),
+            _arg(k_fp8, (torch.uint8, torch.float8_e4m3fn), k_fp8.shape, dev, "k_fp8"),
+            _arg(k_scale, f32, k_scale.shape, dev, "k_scale"), _arg(kv, bf16, kv.shape, dev, "kv"))
+    ctx, st = _on_device(k, stream, "k")
+    with ctx:
+        _raise(load_library().dsa_cache_append(ctypes.byref(shape), _lay(layout), *args, st))
+
+
+def dsa_dense_attn(shape, q, kv, q_pos0, kv_len, out, lse=None, ws=None, ws_bytes=0, stream=None,
+                   layout=None):
+    """Dense attention of the query rows over every latent row they see;
+    ws holds workspace_size(shape, DSA_OP_DENSE_ATTN) bytes."""
+    import torch
+    B, T, H, dev = shape.batch, shape.n_q, shape.heads, q.device
+    bf16, i32 = (torch.bfloat16, torch.int16), (torch.int32,)
+    pool = layout.pool_rows if layout is not None and layout.block_table else B * shape.n_kv
+    if kv.numel() != pool * shape.qk_dim:
+        raise ValueError(f"kv has {kv.numel()} elements, the cache has {pool} rows of {shape.qk_dim}")
+    if ws is not None and ws.device != dev:
+        raise ValueError(f"ws is on {ws.device}, expected {dev}")
+    args = (_arg(q, bf16, (B, T, H, shape.qk_dim), dev, "q"), _arg(kv, bf16, kv.shape, dev, "kv"),
+            _arg(q_pos0, i32, (B,), dev, "q_pos0"), _arg(kv_len, i32, (B,), dev, "kv_len"),
+            _arg(out, (torch.float32, torch.bfloat16), (B, T, H, shape.v_dim), dev, "out"),
+            DSA_OUT_BF16 if out.dtype == torch.bfloat16 else DSA_OUT_F32,
+            _arg(lse, (torch.float32,), (B, T, H), dev, "lse"), _ptr(ws, None, "ws"), int(ws_bytes))
+    ctx, st = _on_device(q, stream, "q")
+    with ctx:
+        _raise(load_library().dsa_dense_attn_ex(ctypes.byref(shape), _lay(layout), *args, st))
 
 
 def dsa_check(stream=None):

@@ -23,6 +23,10 @@
 #include "selftest.cuh"
 #include "quantize.cuh"
 #include "indexer_kl.cuh"
+#include "rope.cuh"
+#include "norm.cuh"
+#include "append.cuh"
+#include "dense_attn.cuh"
 
 namespace {
 
@@ -713,6 +717,270 @@ dsa_status launch_kl_grads(const dsa::KlGradParams& p, int32_t rows, int32_t bat
   return DSA_OK;
 }
 
+// ------------------------------------------------------------------ dense attention
+
+dsa_status check_dense_shape(const dsa_shape* s) {
+  if (dsa_status st = check_shape_common(s)) return st;
+  if (s->qk_dim != 576 || s->v_dim != 512)
+    return fail(DSA_ERR_UNSUPPORTED, "dsa_dense_attn supports (qk_dim, v_dim) = (576, 512) (got %d, %d)",
+                s->qk_dim, s->v_dim);
+  if (s->heads < 1 || s->heads > 128)
+    return fail(DSA_ERR_UNSUPPORTED, "heads must be in [1, 128] (got %d)", s->heads);
+  if (static_cast<int64_t>(s->batch) * s->n_q > 65536)
+    return fail(DSA_ERR_UNSUPPORTED, "dsa_dense_attn takes at most 65536 query rows (got %lld)",
+                static_cast<long long>(s->batch) * s->n_q);
+  if (!std::isfinite(s->softmax_scale) || !(s->softmax_scale > 0.f))
+    return fail(DSA_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+  return DSA_OK;
+}
+
+// Two partial rows (O fp32, LSE) per CTA pair: those that its share's ends cut.
+struct DensePlan {
+  int pairs;
+  size_t o_bytes, total;
+};
+DensePlan plan_dense(const dsa_shape* s) {
+  DensePlan d{};
+  d.pairs = std::max(1, num_sms() / 2);
+  const size_t rows = 2 * static_cast<size_t>(d.pairs) * s->heads;
+  d.o_bytes = (rows * s->v_dim * sizeof(float) + 255) / 256 * 256;
+  d.total = d.o_bytes + (rows * sizeof(float) + 255) / 256 * 256;
+  return d;
+}
+
+// The latent cache as bf16 rows of 576, box 64 dims x 64 rows, 128-byte swizzle.
+dsa_status make_tmap_latent(CUtensorMap* map, const void* base, uint64_t rows) {
+  EncodeTiledFn fn = get_encode_fn();
+  if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  const cuuint64_t dims[2] = {576, rows};
+  const cuuint64_t strides[1] = {1152};
+  const cuuint32_t box[2] = {64, 64};
+  const cuuint32_t estr[2] = {1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
+  return DSA_OK;
+}
+
+dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_t* q,
+                        const uint16_t* kv, const int32_t* q_pos0, const int32_t* kv_len, void* out,
+                        int out_bf16, float* lse, void* ws, cudaStream_t stream, int dev) {
+  using T = dsa::DenseTile;
+  static std::atomic<bool> attr_done[kMaxDevices];
+  if (dsa_status st = set_smem(dsa::dense_attn_kernel, T::SMEM_BYTES, dev, attr_done)) return st;
+  const DensePlan pl = plan_dense(s);
+  dsa::DenseParams p{};
+  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
+  p.km = lay.km;
+  p.rp = dsa::RowPos{q_pos0, lay.row_pos, s->n_q};
+  p.kv_len = kv_len;
+  p.out = out;
+  p.lse = lse;
+  p.part_o = static_cast<float*>(ws);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.o_bytes);
+  p.rows = s->batch * s->n_q;
+  p.n_q = s->n_q;
+  p.n_kv = s->n_kv;
+  p.H = s->heads;
+  p.out_bf16 = out_bf16;
+  p.pairs = pl.pairs;
+  p.min_share = 2;
+  p.scale_log2 = s->softmax_scale * 1.4426950408889634f;
+  CUtensorMap tkv, to, tp;
+  if (dsa_status st = make_tmap_latent(&tkv, kv, static_cast<uint64_t>(lay.km.pool_rows))) return st;
+  if (dsa_status st = make_tmap_rows128(&to, out, static_cast<uint64_t>(p.rows) * p.H,
+                                        static_cast<uint32_t>(s->v_dim) * (out_bf16 ? 2u : 4u),
+                                        static_cast<uint32_t>(p.H)))
+    return st;
+  if (dsa_status st = make_tmap_rows128(&tp, p.part_o, 2ull * pl.pairs * p.H,
+                                        static_cast<uint32_t>(s->v_dim) * 4u,
+                                        static_cast<uint32_t>(p.H)))
+    return st;
+  dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, to, tp, p);
+  DSA_CUDA_TRY(cudaGetLastError(), "dense attention launch");
+  DSA_CUDA_TRY(launch_dependent(dsa::dense_combine_kernel, dim3(p.rows, p.H), dim3(128), 0, stream, p),
+               "dense attention join launch");
+  return DSA_OK;
+}
+
+// ------------------------------------------------------------------ rotary positions
+
+dsa_status check_rope_spec(const dsa_rope_spec* r, const char* what) {
+  if (!r) return fail(DSA_ERR_INVALID_ARG, "%s: rope spec is NULL", what);
+  if (r->rot_dim < 2 || r->rot_dim > 2 * dsa::kRopeMaxPairs || (r->rot_dim & 1))
+    return fail(DSA_ERR_INVALID_ARG, "%s: rot_dim must be even and in [2, 256] (got %d)", what, r->rot_dim);
+  if (r->rot_begin < 0) return fail(DSA_ERR_INVALID_ARG, "%s: rot_begin must be >= 0", what);
+  if (r->layout != DSA_ROPE_HALF && r->layout != DSA_ROPE_INTERLEAVED)
+    return fail(DSA_ERR_INVALID_ARG, "%s: unknown rope layout %d", what, r->layout);
+  if (!std::isfinite(r->amplitude)) return fail(DSA_ERR_INVALID_ARG, "%s: amplitude must be finite", what);
+  for (int i = 0; i < r->rot_dim / 2; ++i)
+    if (!std::isfinite(r->freq[i]))
+      return fail(DSA_ERR_INVALID_ARG, "%s: freq[%d] is not finite", what, i);
+  return DSA_OK;
+}
+
+dsa::RopeAngles rope_angles(const dsa_rope_spec* r) {
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  dsa::RopeAngles a{};
+  a.begin = r->rot_begin;
+  a.pairs = r->rot_dim / 2;
+  a.half = r->layout == DSA_ROPE_HALF;
+  a.amplitude = r->amplitude;
+  for (int i = 0; i < a.pairs; ++i) a.turns[i] = r->freq[i] / kTwoPi;
+  return a;
+}
+
+// Bytes from the first to the end of the last element of a strided tensor.
+int64_t strided_span(const int64_t (&size)[3], const int64_t (&stride)[3], int64_t dim, int64_t esz) {
+  int64_t last = dim;
+  for (int i = 0; i < 3; ++i) last += (size[i] - 1) * stride[i];
+  return last * esz;
+}
+
+// The rows of out (dim elements each) do not overlap one another.
+bool rows_disjoint(const int64_t (&size)[3], const int64_t (&stride)[3], int64_t dim) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return stride[a] < stride[b]; });
+  int64_t extent = dim;
+  for (int i : order) {
+    if (size[i] == 1) continue;
+    if (stride[i] < extent) return false;
+    extent += (size[i] - 1) * stride[i];
+  }
+  return true;
+}
+
+// x and out share no row: their memory is apart, or both have the same
+// strides and the rows of one fall into the gaps of the other.
+bool rows_apart(const void* x, const int64_t (&xs)[3], const void* out, const int64_t (&os)[3],
+                const int64_t (&size)[3], int64_t dim, int64_t esz) {
+  const char* a = static_cast<const char*>(x);
+  const char* b = static_cast<const char*>(out);
+  if (a + strided_span(size, xs, dim, esz) <= b || b + strided_span(size, os, dim, esz) <= a)
+    return true;
+  int64_t g = 0;
+  for (int i = 0; i < 3; ++i) {
+    if (size[i] == 1) continue;
+    if (xs[i] != os[i]) return false;
+    int64_t u = g, v = xs[i];
+    while (v) { const int64_t t = u % v; u = v; v = t; }
+    g = u;
+  }
+  const int64_t d = b - a;
+  if (g == 0 || d % esz) return false;
+  const int64_t off = ((d / esz) % g + g) % g;
+  return off >= dim && off + dim <= g;
+}
+
+template <class T, int E>
+void launch_rope_t(const dsa::RopeParams& p, unsigned grid, int smem, cudaStream_t st) {
+  if (p.a.half) dsa::rope_kernel<T, E, true><<<grid, dsa::kRopeThreads, smem, st>>>(p);
+  else dsa::rope_kernel<T, E, false><<<grid, dsa::kRopeThreads, smem, st>>>(p);
+}
+
+// ------------------------------------------------------------------ layer norm
+
+// Threads per row by width: 8 elements a thread, 16 where that would need
+// the next size of group anyway.
+struct NormPick {
+  int tpr, nv;
+};
+NormPick norm_pick(int dim) {
+  if (dim <= 128) return {16, 1};
+  if (dim <= 256) return {32, 1};
+  if (dim <= 512) return {32, 2};
+  if (dim <= 1024) return {128, 1};
+  if (dim <= 2048) return {128, 2};
+  if (dim <= 4096) return {512, 1};
+  if (dim <= 8192) return {512, 2};
+  return {1024, 2};
+}
+int norm_groups(int tpr) { return tpr <= 32 ? 256 / tpr : 1; }
+
+// CTAs of the two kernels: they walk the rows, so as many as are resident
+// (about 1024 threads per SM for the gradient), fewer when there are few rows.
+unsigned norm_grid(int64_t rows, int dim, int threads_per_sm) {
+  const NormPick k = norm_pick(dim);
+  const int threads = k.tpr <= 32 ? 256 : k.tpr;
+  const int64_t need = (rows + norm_groups(k.tpr) - 1) / norm_groups(k.tpr);
+  const int64_t most = static_cast<int64_t>(num_sms()) * std::max(1, threads_per_sm / threads);
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min(need, most)));
+}
+
+template <bool VEC>
+void launch_norm(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
+  const NormPick k = norm_pick(p.dim);
+  const int threads = k.tpr <= 32 ? 256 : k.tpr;
+  switch (k.tpr * 4 + k.nv) {
+    case 16 * 4 + 1: dsa::norm_kernel<VEC, 16, 1><<<grid, threads, 0, st>>>(p); break;
+    case 32 * 4 + 1: dsa::norm_kernel<VEC, 32, 1><<<grid, threads, 0, st>>>(p); break;
+    case 32 * 4 + 2: dsa::norm_kernel<VEC, 32, 2><<<grid, threads, 0, st>>>(p); break;
+    case 128 * 4 + 1: dsa::norm_kernel<VEC, 128, 1><<<grid, threads, 0, st>>>(p); break;
+    case 128 * 4 + 2: dsa::norm_kernel<VEC, 128, 2><<<grid, threads, 0, st>>>(p); break;
+    case 512 * 4 + 1: dsa::norm_kernel<VEC, 512, 1><<<grid, threads, 0, st>>>(p); break;
+    case 512 * 4 + 2: dsa::norm_kernel<VEC, 512, 2><<<grid, threads, 0, st>>>(p); break;
+    default: dsa::norm_kernel<VEC, 1024, 2><<<grid, threads, 0, st>>>(p); break;
+  }
+}
+template <bool VEC>
+void launch_norm_bwd(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
+  const NormPick k = norm_pick(p.dim);
+  const int threads = k.tpr <= 32 ? 256 : k.tpr;
+  switch (k.tpr * 4 + k.nv) {
+    case 16 * 4 + 1: dsa::norm_bwd_kernel<VEC, 16, 1><<<grid, threads, 0, st>>>(p); break;
+    case 32 * 4 + 1: dsa::norm_bwd_kernel<VEC, 32, 1><<<grid, threads, 0, st>>>(p); break;
+    case 32 * 4 + 2: dsa::norm_bwd_kernel<VEC, 32, 2><<<grid, threads, 0, st>>>(p); break;
+    case 128 * 4 + 1: dsa::norm_bwd_kernel<VEC, 128, 1><<<grid, threads, 0, st>>>(p); break;
+    case 128 * 4 + 2: dsa::norm_bwd_kernel<VEC, 128, 2><<<grid, threads, 0, st>>>(p); break;
+    case 512 * 4 + 1: dsa::norm_bwd_kernel<VEC, 512, 1><<<grid, threads, 0, st>>>(p); break;
+    case 512 * 4 + 2: dsa::norm_bwd_kernel<VEC, 512, 2><<<grid, threads, 0, st>>>(p); break;
+    default: dsa::norm_bwd_kernel<VEC, 1024, 2><<<grid, threads, 0, st>>>(p); break;
+  }
+}
+constexpr int kNormBwdThreadsPerSm = 1024;
+
+dsa_status check_norm_shape(int64_t rows, int32_t dim) {
+  if (rows < 0 || rows > (1ll << 40))
+    return fail(DSA_ERR_INVALID_ARG, "rows must be in [0, 2^40] (got %lld)", static_cast<long long>(rows));
+  if (dim < 1) return fail(DSA_ERR_INVALID_ARG, "dim must be >= 1 (got %d)", dim);
+  if (dim > dsa::kNormMaxDim)
+    return fail(DSA_ERR_UNSUPPORTED, "layer norm supports dim <= %d (got %d)", dsa::kNormMaxDim, dim);
+  return DSA_OK;
+}
+
+// One row tensor of a layer norm call.
+struct NormTensor {
+  const void* p;
+  int32_t dtype;
+  int64_t stride;
+  const char* name;
+};
+dsa_status check_norm_tensor(const NormTensor& t, int64_t rows, int32_t dim, bool written) {
+  if (!t.p) return fail(DSA_ERR_INVALID_ARG, "%s: required pointer is NULL", t.name);
+  if (t.dtype != DSA_F32 && t.dtype != DSA_BF16)
+    return fail(DSA_ERR_INVALID_ARG, "%s: dtype must be DSA_F32 or DSA_BF16", t.name);
+  if (t.stride < 0 || (written && rows > 1 && t.stride < dim) || t.stride > (1ll << 40))
+    return fail(DSA_ERR_INVALID_ARG, "%s: row stride %lld does not fit rows of %d", t.name,
+                static_cast<long long>(t.stride), dim);
+  if (!aligned(t.p, t.dtype == DSA_BF16 ? 2 : 4))
+    return fail(DSA_ERR_INVALID_ARG, "%s is not aligned to its elements", t.name);
+  return DSA_OK;
+}
+bool norm_vec(const NormTensor& t) {
+  return aligned(t.p, 16) && (t.stride * (t.dtype == DSA_BF16 ? 2 : 4)) % 16 == 0;
+}
+// The written tensor is exactly the read one, or shares no byte with it.
+dsa_status check_norm_alias(const NormTensor& in, const NormTensor& out, int64_t rows, int32_t dim) {
+  if (in.p == out.p && in.dtype == out.dtype && (in.stride == out.stride || rows <= 1)) return DSA_OK;
+  const char* a = static_cast<const char*>(in.p);
+  const char* b = static_cast<const char*>(out.p);
+  const int64_t na = ((std::max<int64_t>(rows, 1) - 1) * in.stride + dim) * (in.dtype == DSA_BF16 ? 2 : 4);
+  const int64_t nb = ((std::max<int64_t>(rows, 1) - 1) * out.stride + dim) * (out.dtype == DSA_BF16 ? 2 : 4);
+  if (a + na <= b || b + nb <= a || rows == 0) return DSA_OK;
+  return fail(DSA_ERR_INVALID_ARG, "%s overlaps %s without being the same tensor", out.name, in.name);
+}
+
 dsa_status check_ptrs(std::initializer_list<const void*> ptrs, const char* what) {
   for (const void* p : ptrs)
     if (!p) return fail(DSA_ERR_INVALID_ARG, "%s: required pointer is NULL", what);
@@ -828,6 +1096,11 @@ dsa_status dsa_workspace_size(const dsa_shape* s, int32_t op, size_t* bytes) {
     case DSA_OP_INDEXER_KL: {
       if (dsa_status st = check_kl_shape(s)) return st;
       *bytes = plan_kl(s).total;
+      return DSA_OK;
+    }
+    case DSA_OP_DENSE_ATTN: {
+      if (dsa_status st = check_dense_shape(s)) return st;
+      *bytes = plan_dense(s).total;
       return DSA_OK;
     }
     default:
@@ -1148,6 +1421,325 @@ dsa_status dsa_indexer_kl(const dsa_shape* s, const uint8_t* q_fp8, const float*
   return DSA_OK;
 }
 
+dsa_status dsa_dense_attn_ex(const dsa_shape* s, const dsa_layout* layout, const uint16_t* q,
+                             const uint16_t* kv, const int32_t* q_pos0, const int32_t* kv_len,
+                             void* out, int32_t out_dtype, float* lse, void* ws, size_t ws_bytes,
+                             void* stream) {
+  if (dsa_status st = check_dense_shape(s)) return st;
+  if (dsa_status st = check_ptrs({q, kv, out}, "dsa_dense_attn")) return st;
+  if (out_dtype != DSA_OUT_F32 && out_dtype != DSA_OUT_BF16)
+    return fail(DSA_ERR_INVALID_ARG, "out_dtype must be DSA_OUT_F32 or DSA_OUT_BF16");
+  if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(out, 16))
+    return fail(DSA_ERR_INVALID_ARG, "q, kv and out must be 16-byte aligned");
+  if (!aligned(q_pos0, 4) || !aligned(kv_len, 4) || !aligned(lse, 4))
+    return fail(DSA_ERR_INVALID_ARG, "q_pos0, kv_len and lse must be 4-byte aligned");
+  HostLayout lay;
+  if (dsa_status st = resolve_layout(s, layout, &lay)) return st;
+  const DensePlan pl = plan_dense(s);
+  if (!ws || ws_bytes < pl.total)
+    return fail(DSA_ERR_WORKSPACE, "dsa_dense_attn needs %zu workspace bytes, got %zu", pl.total,
+                ws ? ws_bytes : size_t(0));
+  if (!aligned(ws, 256)) return fail(DSA_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  int dev;
+  if (dsa_status st = current_device(&dev)) return st;
+  return launch_dense(s, lay, q, kv, q_pos0, kv_len, out, out_dtype == DSA_OUT_BF16, lse, ws,
+                      static_cast<cudaStream_t>(stream), dev);
+}
+
+dsa_status dsa_dense_attn(const dsa_shape* s, const uint16_t* q, const uint16_t* kv,
+                          const int32_t* q_pos0, const int32_t* kv_len, void* out,
+                          int32_t out_dtype, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  return dsa_dense_attn_ex(s, nullptr, q, kv, q_pos0, kv_len, out, out_dtype, lse, ws, ws_bytes,
+                           stream);
+}
+
+dsa_status dsa_rope_init(dsa_rope_spec* r, int32_t rot_dim, int32_t rot_begin, int32_t layout,
+                         double base, int32_t scaling, double factor, int32_t orig_context,
+                         double beta_fast, double beta_slow, float amplitude) {
+  if (!r) return fail(DSA_ERR_INVALID_ARG, "dsa_rope_init: rope spec is NULL");
+  dsa_rope_spec t{};
+  t.rot_dim = rot_dim;
+  t.rot_begin = rot_begin;
+  t.layout = layout;
+  t.amplitude = amplitude;
+  if (dsa_status st = check_rope_spec(&t, "dsa_rope_init")) return st;
+  if (!std::isfinite(base) || !(base > 0.0))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope_init: base must be finite and > 0");
+  if (scaling != DSA_ROPE_PLAIN && scaling != DSA_ROPE_LINEAR && scaling != DSA_ROPE_YARN)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope_init: unknown scaling %d", scaling);
+  if (scaling != DSA_ROPE_PLAIN && (!std::isfinite(factor) || !(factor > 0.0)))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope_init: factor must be finite and > 0");
+  if (scaling == DSA_ROPE_YARN && (orig_context < 1 || !std::isfinite(beta_fast) ||
+                                   !std::isfinite(beta_slow) || !(beta_fast > beta_slow)))
+    return fail(DSA_ERR_INVALID_ARG,
+                "dsa_rope_init: YaRN needs orig_context >= 1 and beta_fast > beta_slow");
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / rot_dim);
+    if (scaling == DSA_ROPE_LINEAR) {
+      f /= factor;
+    } else if (scaling == DSA_ROPE_YARN) {
+      const double turns = orig_context * f / kTwoPi;
+      const double g = std::min(1.0, std::max(0.0, (turns - beta_slow) / (beta_fast - beta_slow)));
+      f = (1.0 - g) * f / factor + g * f;
+    }
+    t.freq[i] = f;
+  }
+  *r = t;
+  return DSA_OK;
+}
+
+dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* v, const void* x, void* out,
+                    const int32_t* q_pos0, const int32_t* row_pos, int32_t backward, void* stream) {
+  if (dsa_status st = check_rope_spec(spec, "dsa_rope")) return st;
+  if (!v) return fail(DSA_ERR_INVALID_ARG, "dsa_rope: view is NULL");
+  if (dsa_status st = check_ptrs({x, out}, "dsa_rope")) return st;
+  if (v->dtype != DSA_F32 && v->dtype != DSA_BF16)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: dtype must be DSA_F32 or DSA_BF16");
+  if (v->batch < 1 || v->n_q < 1 || v->heads < 1 || v->dim < 1 || v->dim > 65536)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: sizes must be >= 1 and dim <= 65536 (got %d, %d, %d, %d)",
+                v->batch, v->n_q, v->heads, v->dim);
+  const int64_t tokens = static_cast<int64_t>(v->batch) * v->n_q;
+  if (tokens * v->heads >= (1ll << 31) || tokens >= (1ll << 31))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: batch * n_q * heads must be below 2^31");
+  if (spec->rot_begin > v->dim - spec->rot_dim)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: dims [%d, %d) lie outside the head's %d", spec->rot_begin,
+                spec->rot_begin + spec->rot_dim, v->dim);
+  const int esz = v->dtype == DSA_BF16 ? 2 : 4;
+  if (!aligned(x, esz) || !aligned(out, esz) || !aligned(q_pos0, 4) || !aligned(row_pos, 4))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: pointers must be aligned to their elements");
+  const int64_t size[3] = {v->batch, v->n_q, v->heads};
+  dsa::RopeParams p{};
+  bool same = x == out;
+  for (int i = 0; i < 3; ++i) {
+    if (v->x_stride[i] < 0 || v->out_stride[i] < 0 || v->x_stride[i] > (1ll << 40) ||
+        v->out_stride[i] > (1ll << 40))
+      return fail(DSA_ERR_INVALID_ARG, "dsa_rope: strides must be in [0, 2^40]");
+    // the stride of a single entry plays no part
+    p.xs[i] = size[i] == 1 ? 0 : v->x_stride[i];
+    p.os[i] = size[i] == 1 ? 0 : v->out_stride[i];
+    same = same && p.xs[i] == p.os[i];
+  }
+  if (!rows_disjoint(size, p.os, v->dim))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: rows of out overlap one another");
+  if (!same && !rows_apart(x, p.xs, out, p.os, size, v->dim, esz))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_rope: out overlaps x without being the same tensor");
+  p.x = x;
+  p.out = out;
+  p.rp = dsa::RowPos{q_pos0, row_pos, v->n_q};
+  p.rows = static_cast<uint32_t>(tokens * v->heads);
+  p.heads = v->heads;
+  p.n_q = v->n_q;
+  p.dim = v->dim;
+  p.copy = !same;
+  p.sign = backward ? -1.f : 1.f;
+  p.by_heads = dsa::FastDiv::make(static_cast<uint32_t>(v->heads));
+  p.by_tokens = dsa::FastDiv::make(static_cast<uint32_t>(v->n_q));
+  p.a = rope_angles(spec);
+  // 16-byte chunks when every chunk of every row starts on one
+  const int e = 16 / esz;
+  bool vec = aligned(x, 16) && aligned(out, 16) && p.a.begin % e == 0 &&
+             (p.a.half ? p.a.pairs : 2 * p.a.pairs) % e == 0 && (same || v->dim % e == 0);
+  for (int i = 0; i < 3; ++i) vec = vec && p.xs[i] % e == 0 && p.os[i] % e == 0;
+  // Rows per CTA: what its threads hold in one unrolled step, times up to
+  // four while every SM keeps several CTAs; fewer when the tokens' cos and sin
+  // would not fit (one token more than the rows' share may be touched at each end).
+  const int per_item = vec ? (p.a.half ? e : e / 2) : 1;
+  const int lanes = std::max(1, dsa::kRopeThreads / (p.a.pairs / per_item));
+  const int64_t cap = std::min<int64_t>(dsa::kRopeMaxTokens, dsa::kRopeTableBytes / (8 * p.a.pairs));
+  int64_t per_cta = lanes;
+  while (per_cta < 16 * lanes && p.rows / (2 * per_cta) >= 8ll * num_sms()) per_cta *= 2;
+  per_cta = std::max<int64_t>(1, std::min(per_cta, (cap - 2) * v->heads));
+  p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(per_cta, 1 << 20));
+  const int64_t touched = std::min<int64_t>(tokens, (p.rows_per_cta - 1) / v->heads + 2);
+  const int smem = static_cast<int>(touched * p.a.pairs * 8);
+  const unsigned grid = (p.rows + p.rows_per_cta - 1) / static_cast<uint32_t>(p.rows_per_cta);
+  int dev;
+  if (dsa_status st = current_device(&dev)) return st;
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (v->dtype == DSA_BF16) {
+    if (vec) launch_rope_t<__nv_bfloat16, 8>(p, grid, smem, st_);
+    else launch_rope_t<__nv_bfloat16, 1>(p, grid, smem, st_);
+  } else {
+    if (vec) launch_rope_t<float, 4>(p, grid, smem, st_);
+    else launch_rope_t<float, 1>(p, grid, smem, st_);
+  }
+  DSA_CUDA_TRY(cudaGetLastError(), "rotary positions launch");
+  return DSA_OK;
+}
+
+dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype,
+                         int64_t x_stride, const float* weight, const float* bias, float eps,
+                         void* y, int32_t y_dtype, int64_t y_stride, float* mean, float* rstd,
+                         void* stream) {
+  if (dsa_status st = check_norm_shape(rows, dim)) return st;
+  const NormTensor tx{x, x_dtype, x_stride, "dsa_layernorm: x"}, ty{y, y_dtype, y_stride, "dsa_layernorm: y"};
+  if (dsa_status st = check_norm_tensor(tx, rows, dim, false)) return st;
+  if (dsa_status st = check_norm_tensor(ty, rows, dim, true)) return st;
+  if (dsa_status st = check_norm_alias(tx, ty, rows, dim)) return st;
+  if (!std::isfinite(eps) || eps < 0.f)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_layernorm: eps must be finite and >= 0");
+  if (!aligned(weight, 4) || !aligned(bias, 4) || !aligned(mean, 4) || !aligned(rstd, 4))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_layernorm: fp32 arrays must be 4-byte aligned");
+  if (rows == 0) return DSA_OK;
+  int dev;
+  if (dsa_status st = current_device(&dev)) return st;
+  dsa::NormParams p{};
+  p.x = x;
+  p.w = weight;
+  p.b = bias;
+  p.y = y;
+  p.mean = mean;
+  p.rstd = rstd;
+  p.rows = rows;
+  p.xs = x_stride;
+  p.ys = y_stride;
+  p.dim = dim;
+  p.x_bf16 = x_dtype == DSA_BF16;
+  p.y_bf16 = y_dtype == DSA_BF16;
+  p.eps = eps;
+  const unsigned grid = norm_grid(rows, dim, 2048);
+  if (dim % 8 == 0 && norm_vec(tx) && norm_vec(ty)) launch_norm<true>(p, grid, static_cast<cudaStream_t>(stream));
+  else launch_norm<false>(p, grid, static_cast<cudaStream_t>(stream));
+  DSA_CUDA_TRY(cudaGetLastError(), "layer norm launch");
+  return DSA_OK;
+}
+
+dsa_status dsa_layernorm_bwd_workspace(int64_t rows, int32_t dim, size_t* bytes) {
+  if (!bytes) return fail(DSA_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = 0;
+  if (dsa_status st = check_norm_shape(rows, dim)) return st;
+  if (rows > 0)
+    *bytes = static_cast<size_t>(norm_grid(rows, dim, kNormBwdThreadsPerSm)) * 2 * dim * sizeof(float);
+  return DSA_OK;
+}
+
+dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t dy_dtype,
+                             int64_t dy_stride, const void* x, int32_t x_dtype, int64_t x_stride,
+                             const float* weight, const float* mean, const float* rstd, void* dx,
+                             int32_t dx_dtype, int64_t dx_stride, float* dweight, float* dbias,
+                             void* ws, size_t ws_bytes, void* stream) {
+  if (dsa_status st = check_norm_shape(rows, dim)) return st;
+  const NormTensor tdy{dy, dy_dtype, dy_stride, "dsa_layernorm_bwd: dy"},
+      tx{x, x_dtype, x_stride, "dsa_layernorm_bwd: x"}, tdx{dx, dx_dtype, dx_stride, "dsa_layernorm_bwd: dx"};
+  if (dsa_status st = check_norm_tensor(tdy, rows, dim, false)) return st;
+  if (dsa_status st = check_norm_tensor(tx, rows, dim, false)) return st;
+  if (dsa_status st = check_norm_tensor(tdx, rows, dim, true)) return st;
+  if (dsa_status st = check_norm_alias(tdy, tdx, rows, dim)) return st;
+  if (dsa_status st = check_norm_alias(tx, tdx, rows, dim)) return st;
+  if (dsa_status st = check_ptrs({mean, rstd}, "dsa_layernorm_bwd")) return st;
+  if (!aligned(weight, 4) || !aligned(mean, 4) || !aligned(rstd, 4) || !aligned(dweight, 4) ||
+      !aligned(dbias, 4))
+    return fail(DSA_ERR_INVALID_ARG, "dsa_layernorm_bwd: fp32 arrays must be 4-byte aligned");
+  const bool sums = dweight || dbias;
+  const unsigned grid = norm_grid(rows, dim, kNormBwdThreadsPerSm);
+  const size_t need = sums && rows > 0 ? static_cast<size_t>(grid) * 2 * dim * sizeof(float) : 0;
+  if (need > 0) {
+    if (!ws || ws_bytes < need)
+      return fail(DSA_ERR_WORKSPACE, "dsa_layernorm_bwd needs %zu workspace bytes, got %zu", need,
+                  ws ? ws_bytes : size_t(0));
+    if (!aligned(ws, 16)) return fail(DSA_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+  }
+  if (rows == 0 && !sums) return DSA_OK;
+  int dev;
+  if (dsa_status st = current_device(&dev)) return st;
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  float* part = static_cast<float*>(ws);
+  if (rows > 0) {
+    dsa::NormBwdParams p{};
+    p.dy = dy;
+    p.x = x;
+    p.w = weight;
+    p.mean = mean;
+    p.rstd = rstd;
+    p.dx = dx;
+    p.part = sums ? part : nullptr;
+    p.rows = rows;
+    p.dys = dy_stride;
+    p.xs = x_stride;
+    p.dxs = dx_stride;
+    p.dim = dim;
+    p.dy_bf16 = dy_dtype == DSA_BF16;
+    p.x_bf16 = x_dtype == DSA_BF16;
+    p.dx_bf16 = dx_dtype == DSA_BF16;
+    if (dim % 8 == 0 && norm_vec(tdy) && norm_vec(tx) && norm_vec(tdx)) launch_norm_bwd<true>(p, grid, st_);
+    else launch_norm_bwd<false>(p, grid, st_);
+    DSA_CUDA_TRY(cudaGetLastError(), "layer norm gradient launch");
+  }
+  if (sums) {
+    const dim3 rgrid((2 * dim + 31) / 32);
+    const int n = rows > 0 ? static_cast<int>(grid) : 0;
+    if (rows > 0)
+      DSA_CUDA_TRY(launch_dependent(dsa::norm_bwd_reduce_kernel, rgrid, dim3(1024), 0, st_,
+                                    static_cast<const float*>(part), dweight, dbias, dim, n),
+                   "layer norm weight gradient launch");
+    else
+      dsa::norm_bwd_reduce_kernel<<<rgrid, 1024, 0, st_>>>(part, dweight, dbias, dim, n);
+    DSA_CUDA_TRY(cudaGetLastError(), "layer norm weight gradient launch");
+  }
+  return DSA_OK;
+}
+
+dsa_status dsa_cache_append(const dsa_shape* s, const dsa_layout* layout, const uint16_t* k,
+                            const float* ln_weight, const float* ln_bias, float eps,
+                            const dsa_rope_spec* idx_rope, const uint16_t* c,
+                            const dsa_rope_spec* kv_rope, const int32_t* q_pos0,
+                            const int32_t* n_new, uint8_t* k_fp8, float* k_scale, uint16_t* kv,
+                            void* stream) {
+  if (dsa_status st = check_shape_common(s)) return st;
+  if ((s->idx_dim != 32 && s->idx_dim != 128) || (s->qk_dim != 64 && s->qk_dim != 576))
+    return fail(DSA_ERR_UNSUPPORTED,
+                "dsa_cache_append supports idx_dim 32 or 128 and qk_dim 64 or 576 (got %d, %d)",
+                s->idx_dim, s->qk_dim);
+  if (dsa_status st = check_rope_spec(idx_rope, "dsa_cache_append: key")) return st;
+  if (dsa_status st = check_rope_spec(kv_rope, "dsa_cache_append: latent row")) return st;
+  if (idx_rope->rot_begin > s->idx_dim - idx_rope->rot_dim || kv_rope->rot_begin > s->qk_dim - kv_rope->rot_dim)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_cache_append: rotated dims lie outside the rows");
+  if (dsa_status st = check_ptrs({k, c, k_fp8, k_scale, kv}, "dsa_cache_append")) return st;
+  if (!std::isfinite(eps) || eps < 0.f)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_cache_append: eps must be finite and >= 0");
+  if (!aligned(k, 8) || !aligned(c, 16) || !aligned(kv, 16) || !aligned(k_fp8, 4))
+    return fail(DSA_ERR_INVALID_ARG, "k must be 8-byte, c and kv 16-byte, k_fp8 4-byte aligned");
+  if (!aligned(ln_weight, 4) || !aligned(ln_bias, 4) || !aligned(k_scale, 4) || !aligned(q_pos0, 4) ||
+      !aligned(n_new, 4))
+    return fail(DSA_ERR_INVALID_ARG, "fp32 and int32 arrays must be 4-byte aligned");
+  if (layout && layout->row_pos)
+    return fail(DSA_ERR_INVALID_ARG, "dsa_cache_append: row_pos must be NULL (use q_pos0)");
+  HostLayout lay;
+  if (dsa_status st = resolve_layout(s, layout, &lay)) return st;
+  int dev;
+  if (dsa_status st = current_device(&dev)) return st;
+  dsa::AppendParams p{};
+  p.k = reinterpret_cast<const __nv_bfloat16*>(k);
+  p.c = reinterpret_cast<const __nv_bfloat16*>(c);
+  p.w = ln_weight;
+  p.b = ln_bias;
+  p.q_pos0 = q_pos0;
+  p.n_new = n_new;
+  p.k_fp8 = k_fp8;
+  p.k_scale = k_scale;
+  p.kv = reinterpret_cast<__nv_bfloat16*>(kv);
+  p.km = lay.km;
+  p.n_q = s->n_q;
+  p.n_kv = s->n_kv;
+  p.tokens = static_cast<long long>(s->batch) * s->n_q;
+  p.eps = eps;
+  p.ak = rope_angles(idx_rope);
+  p.ac = rope_angles(kv_rope);
+  const unsigned grid = static_cast<unsigned>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps);
+  constexpr int threads = 32 * dsa::kAppendWarps;
+  cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (s->idx_dim == 128) {
+    if (s->qk_dim == 576) dsa::append_kernel<128, 576><<<grid, threads, 0, st_>>>(p);
+    else dsa::append_kernel<128, 64><<<grid, threads, 0, st_>>>(p);
+  } else {
+    if (s->qk_dim == 576) dsa::append_kernel<32, 576><<<grid, threads, 0, st_>>>(p);
+    else dsa::append_kernel<32, 64><<<grid, threads, 0, st_>>>(p);
+  }
+  DSA_CUDA_TRY(cudaGetLastError(), "cache append launch");
+  return DSA_OK;
+}
+
 dsa_status dsa_check(void* stream) {
   cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "stream synchronize");
@@ -1163,8 +1755,8 @@ dsa_status dsa_check(void* stream) {
       return fail(DSA_ERR_CUDA, "a kernel invariant failed (error word 0x%x)", word);
     if (word & dsa::kErrBadInput)
       return fail(DSA_ERR_INVALID_ARG,
-                  "a block-table page was outside the key pool; its keys were skipped "
-                  "(error word 0x%x)",
+                  "a block-table page was outside the key pool, or an append past its cache; its "
+                  "keys were skipped (error word 0x%x)",
                   word);
     return fail(DSA_ERR_CUDA, "device error word 0x%x", word);
   }
