@@ -11,6 +11,8 @@ from __future__ import annotations
 import ctypes
 import os
 
+import torch
+
 from .inputs import CONFIGS, DsaConfig, custom_config, make_inputs  # noqa: F401
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -357,46 +359,56 @@ def indexer_kl(inp: dict, cfg: DsaConfig, stream=None):
 
 # ------------------------------------------------------------------ next to the path
 
-def _on_device(t, stream, what="tensor"):
-    """(context manager, raw stream) of a launch on t's device: that device is
-    made current for the call, and None means its current stream."""
-    import contextlib
+# These calls are short next to their launches (a decode step makes several),
+# so the checks below read each tensor property once and build nothing.
+_F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
+_BITS16, _CODES = (torch.bfloat16, torch.int16), (torch.uint8, torch.float8_e4m3fn)
+_FLOATS = (torch.float32, torch.bfloat16)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    idx = t.device.index
-    here = torch.cuda.current_device() == idx
+
+def _launch(fn, idx, stream, *args):
+    """Calls fn(*args, stream) with CUDA device idx current (stream None: that
+    device's current stream) and raises on a status."""
+    if idx < 0:
+        raise ValueError("tensors must be on a CUDA device")
     if stream is None:
-        stream = torch.cuda.current_stream(idx).cuda_stream
+        stream = (_raw_stream(idx) if _raw_stream is not None
+                  else torch.cuda.current_stream(idx).cuda_stream)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    return (contextlib.nullcontext() if here else torch.cuda.device(idx)), stream
+    if torch.cuda.current_device() == idx:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(idx):
+            status = fn(*args, stream)
+    if status != DSA_OK:
+        _raise(status)
 
 
-def _arg(t, dtypes, shape, device, what):
+def _arg(t, dtypes, shape, idx, what):
     """Raw pointer of a contiguous tensor of the given dtypes and shape on
-    `device` (None -> NULL)."""
+    CUDA device idx (None -> NULL; shape None: any)."""
     if t is None:
         return None
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise ValueError(f"{what} has dtype {t.dtype}, expected one of {dtypes}")
-    if tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.get_device() != idx:
+        raise ValueError(f"{what} is on {t.device}, expected device {idx}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
 
 
 def _dtype_code(t, what):
-    import torch
-    if t.dtype == torch.bfloat16:
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return DSA_BF16
-    if t.dtype == torch.float32:
+    if dt is torch.float32:
         return DSA_F32
-    raise ValueError(f"{what} has dtype {t.dtype}, expected bfloat16 or float32")
+    raise ValueError(f"{what} has dtype {dt}, expected bfloat16 or float32")
 
 
 def rope_spec(rot_dim, rot_begin=0, layout=DSA_ROPE_HALF, base=10000.0, scaling=DSA_ROPE_PLAIN,
@@ -415,57 +427,61 @@ def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=Non
     """Rotary positions: out = x [B, T, H, D] (bf16 or fp32, any strides, D
     contiguous) with the spec's dims turned by each token's position; out may
     be x. backward applies the transpose."""
-    import torch
-    if x.dim() != 4 or x.shape != out.shape:
+    shape, dev = x.shape, x.get_device()
+    if len(shape) != 4 or shape != out.shape:
         raise ValueError("x and out must be [B, T, H, D] of the same shape")
-    if x.dtype != out.dtype or x.device != out.device:
+    if x.dtype != out.dtype or dev != out.get_device():
         raise ValueError("x and out must have the same dtype and device")
-    B, T, H, D = x.shape
+    B, T, H, D = shape
     xs, os_ = x.stride(), out.stride()
     if D > 1 and (xs[3] != 1 or os_[3] != 1):
         raise ValueError("the last dim of x and out must be contiguous")
     code = _dtype_code(x, "x")
-    p0 = _arg(q_pos0, (torch.int32,), (B,), x.device, "q_pos0")
-    rp = _arg(row_pos, (torch.int32,), (B, T), x.device, "row_pos")
-    ctx, st = _on_device(x, stream, "x")
-    if x.numel() == 0:
+    p0 = _arg(q_pos0, _I32, (B,), dev, "q_pos0")
+    rp = _arg(row_pos, _I32, (B, T), dev, "row_pos")
+    if dev >= 0 and 0 in shape:
         return
     view = DsaRopeView(B, T, H, D, code, xs[:3], os_[:3])
-    with ctx:
-        _raise(load_library().dsa_rope(ctypes.byref(spec), ctypes.byref(view), x.data_ptr(),
-                                       out.data_ptr(), p0, rp, 1 if backward else 0, st))
+    _launch(load_library().dsa_rope, dev, stream, spec, view, x.data_ptr(), out.data_ptr(), p0, rp,
+            1 if backward else 0)
 
 
 def _rows(t, what):
     """(rows, dim, row stride) of a tensor [..., dim] whose rows are evenly
     spaced: contiguous, or a 2-D tensor with any row stride."""
-    if t.dim() == 2 and (t.shape[1] == 1 or t.stride(1) == 1):
-        return t.shape[0], t.shape[1], t.stride(0)
-    if t.dim() < 1 or not t.is_contiguous():
+    shape = t.shape
+    if len(shape) == 2:
+        st = t.stride()
+        if shape[1] == 1 or st[1] == 1:
+            return shape[0], shape[1], st[0]
+    if len(shape) < 1 or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous, or 2-D with contiguous rows")
-    dim = t.shape[-1]
+    dim = shape[-1]
     return (t.numel() // dim if dim else 0), dim, dim
+
+
+def _row_stat(t, rows, idx, what):
+    """Pointer of an fp32 tensor with one element per row, in any shape."""
+    if t is not None and t.numel() != rows:
+        raise ValueError(f"{what} has {t.numel()} elements, expected {rows}")
+    return _arg(t, _F32, None, idx, what)
 
 
 def dsa_layernorm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
     """Layer norm over the last dim of x into y (bf16 or fp32 each); weight and
     bias fp32 [dim] or None; mean and rstd fp32 [rows] receive the statistics."""
-    import torch
     rows, dim, xs = _rows(x, "x")
-    f32, dev = (torch.float32,), x.device
-    if x.shape != y.shape or y.device != dev:
+    dev = x.get_device()
+    if x.shape != y.shape or y.get_device() != dev:
         raise ValueError("y must have x's shape and device")
-    _, _, ys = _rows(y, "y")
+    ys = _rows(y, "y")[2]
     xc, yc = _dtype_code(x, "x"), _dtype_code(y, "y")
-    w, b = _arg(weight, f32, (dim,), dev, "weight"), _arg(bias, f32, (dim,), dev, "bias")
-    stats = [None if t is None else _arg(t, f32, t.shape if t.numel() == rows else (rows,), dev, n)
-             for t, n in ((mean, "mean"), (rstd, "rstd"))]
-    ctx, st = _on_device(x, stream, "x")
-    if rows == 0:
+    w, b = _arg(weight, _F32, (dim,), dev, "weight"), _arg(bias, _F32, (dim,), dev, "bias")
+    m, r = _row_stat(mean, rows, dev, "mean"), _row_stat(rstd, rows, dev, "rstd")
+    if rows == 0 and dev >= 0:
         return
-    with ctx:
-        _raise(load_library().dsa_layernorm(rows, dim, x.data_ptr(), xc, xs, w, b, float(eps),
-                                            y.data_ptr(), yc, ys, stats[0], stats[1], st))
+    _launch(load_library().dsa_layernorm, dev, stream, rows, dim, x.data_ptr(), xc, xs, w, b, eps,
+            y.data_ptr(), yc, ys, m, r)
 
 
 def layernorm_bwd_workspace(rows: int, dim: int) -> int:
@@ -478,29 +494,27 @@ def dsa_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, w
                       ws_bytes=0, stream=None):
     """Gradient of dsa_layernorm: dx (bf16 or fp32), and dweight, dbias (fp32
     [dim], may be None). ws holds layernorm_bwd_workspace(rows, dim) bytes."""
-    import torch
     rows, dim, xs = _rows(x, "x")
-    f32, dev = (torch.float32,), x.device
-    for t, n in ((dy, "dy"), (dx, "dx")):
-        if t.shape != x.shape or t.device != dev:
-            raise ValueError(f"{n} must have x's shape and device")
-    _, _, dys = _rows(dy, "dy")
-    _, _, dxs = _rows(dx, "dx")
-    codes = _dtype_code(dy, "dy"), _dtype_code(x, "x"), _dtype_code(dx, "dx")
-    w = _arg(weight, f32, (dim,), dev, "weight")
-    stats = [_arg(t, f32, t.shape if t.numel() == rows else (rows,), dev, n)
-             for t, n in ((mean, "mean"), (rstd, "rstd"))]
-    dw, db = _arg(dweight, f32, (dim,), dev, "dweight"), _arg(dbias, f32, (dim,), dev, "dbias")
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
-    ctx, st = _on_device(x, stream, "x")
-    with ctx:
-        # an empty tensor has no address; with no rows nothing is read through it
-        some = (lambda t: t.data_ptr() or 256) if rows == 0 else (lambda t: t.data_ptr())
-        _raise(load_library().dsa_layernorm_bwd(
-            rows, dim, some(dy), codes[0], dys, some(x), codes[1], xs, w,
-            stats[0] or (256 if rows == 0 else None), stats[1] or (256 if rows == 0 else None),
-            some(dx), codes[2], dxs, dw, db, _ptr(ws, None, "ws"), int(ws_bytes), st))
+    shape, dev = x.shape, x.get_device()
+    if dy.shape != shape or dx.shape != shape or dy.get_device() != dev or dx.get_device() != dev:
+        raise ValueError("dy and dx must have x's shape and device")
+    dys, dxs = _rows(dy, "dy")[2], _rows(dx, "dx")[2]
+    dyc, xc, dxc = _dtype_code(dy, "dy"), _dtype_code(x, "x"), _dtype_code(dx, "dx")
+    w = _arg(weight, _F32, (dim,), dev, "weight")
+    m, r = _row_stat(mean, rows, dev, "mean"), _row_stat(rstd, rows, dev, "rstd")
+    dw, db = _arg(dweight, _F32, (dim,), dev, "dweight"), _arg(dbias, _F32, (dim,), dev, "dbias")
+    wp = _arg(ws, (torch.uint8,), None, dev, "ws")
+    ptrs = [dy.data_ptr(), x.data_ptr(), dx.data_ptr(), m, r]
+    if rows == 0:      # empty tensors have no address, and nothing is read through one
+        ptrs = [256] * 5
+    _launch(load_library().dsa_layernorm_bwd, dev, stream, rows, dim, ptrs[0], dyc, dys, ptrs[1], xc,
+            xs, w, ptrs[3], ptrs[4], ptrs[2], dxc, dxs, dw, db, wp, ws_bytes)
+
+
+def _pool_rows(shape, layout):
+    if layout is not None and layout.block_table:
+        return layout.pool_rows
+    return shape.batch * shape.n_kv
 
 
 def dsa_cache_append(shape, k, ln_weight, ln_bias, eps, idx_rope, c, kv_rope, q_pos0, n_new,
@@ -509,45 +523,32 @@ def dsa_cache_append(shape, k, ln_weight, ln_bias, eps, idx_rope, c, kv_rope, q_
     norm, rotation and row encoding into k_fp8 / k_scale, latent rows c
     [B, T, D_qk] bf16 by rotation into kv, at positions q_pos0[b] + i for
     i < n_new[b]."""
-    import torch
-    B, T, dev = shape.batch, shape.n_q, k.device
-    f32, i32, bf16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
-    pool = layout.pool_rows if layout is not None and layout.block_table else B * shape.n_kv
-    for t, per, n in ((k_fp8, shape.idx_dim, "k_fp8"), (k_scale, 1, "k_scale"), (kv, shape.qk_dim, "kv")):
-        if t.numel() != pool * per:
-            raise ValueError(f"{n} has {t.numel()} elements, the cache has {pool} rows of {per}")
-    args = (_arg(k, bf16, (B, T, shape.idx_dim), dev, "k"),
-            _arg(ln_weight, f32, (shape.idx_dim,), dev, "ln_weight"),
-            _arg(ln_bias, f32, (shape.idx_dim,), dev, "ln_bias"), float(eps), ctypes.byref(idx_rope),
-            _arg(c, bf16, (B, T, shape.qk_dim), dev, "c"), ctypes.byref(kv_rope),
-            _arg(q_pos0, i32, (B,), dev, "q_pos0"), _arg(n_new, i32, (B,), dev, "n_new"),
-            _arg(k_fp8, (torch.uint8, torch.float8_e4m3fn), k_fp8.shape, dev, "k_fp8"),
-            _arg(k_scale, f32, k_scale.shape, dev, "k_scale"), _arg(kv, bf16, kv.shape, dev, "kv"))
-    ctx, st = _on_device(k, stream, "k")
-    with ctx:
-        _raise(load_library().dsa_cache_append(ctypes.byref(shape), _lay(layout), *args, st))
+    B, T, di, dq, dev = shape.batch, shape.n_q, shape.idx_dim, shape.qk_dim, k.get_device()
+    pool = _pool_rows(shape, layout)
+    if k_fp8.numel() != pool * di or k_scale.numel() != pool or kv.numel() != pool * dq:
+        raise ValueError(f"k_fp8, k_scale and kv must have {pool} rows of {di}, 1 and {dq} elements")
+    _launch(load_library().dsa_cache_append, dev, stream, shape, layout,
+            _arg(k, _BF16, (B, T, di), dev, "k"), _arg(ln_weight, _F32, (di,), dev, "ln_weight"),
+            _arg(ln_bias, _F32, (di,), dev, "ln_bias"), eps, idx_rope,
+            _arg(c, _BF16, (B, T, dq), dev, "c"), kv_rope, _arg(q_pos0, _I32, (B,), dev, "q_pos0"),
+            _arg(n_new, _I32, (B,), dev, "n_new"), _arg(k_fp8, _CODES, None, dev, "k_fp8"),
+            _arg(k_scale, _F32, None, dev, "k_scale"), _arg(kv, _BITS16, None, dev, "kv"))
 
 
 def dsa_dense_attn(shape, q, kv, q_pos0, kv_len, out, lse=None, ws=None, ws_bytes=0, stream=None,
                    layout=None):
     """Dense attention of the query rows over every latent row they see;
     ws holds workspace_size(shape, DSA_OP_DENSE_ATTN) bytes."""
-    import torch
-    B, T, H, dev = shape.batch, shape.n_q, shape.heads, q.device
-    bf16, i32 = (torch.bfloat16, torch.int16), (torch.int32,)
-    pool = layout.pool_rows if layout is not None and layout.block_table else B * shape.n_kv
-    if kv.numel() != pool * shape.qk_dim:
-        raise ValueError(f"kv has {kv.numel()} elements, the cache has {pool} rows of {shape.qk_dim}")
-    if ws is not None and ws.device != dev:
-        raise ValueError(f"ws is on {ws.device}, expected {dev}")
-    args = (_arg(q, bf16, (B, T, H, shape.qk_dim), dev, "q"), _arg(kv, bf16, kv.shape, dev, "kv"),
-            _arg(q_pos0, i32, (B,), dev, "q_pos0"), _arg(kv_len, i32, (B,), dev, "kv_len"),
-            _arg(out, (torch.float32, torch.bfloat16), (B, T, H, shape.v_dim), dev, "out"),
+    B, T, H, dq, dev = shape.batch, shape.n_q, shape.heads, shape.qk_dim, q.get_device()
+    pool = _pool_rows(shape, layout)
+    if kv.numel() != pool * dq:
+        raise ValueError(f"kv has {kv.numel()} elements, the cache has {pool} rows of {dq}")
+    _launch(load_library().dsa_dense_attn_ex, dev, stream, shape, layout,
+            _arg(q, _BITS16, (B, T, H, dq), dev, "q"), _arg(kv, _BITS16, None, dev, "kv"),
+            _arg(q_pos0, _I32, (B,), dev, "q_pos0"), _arg(kv_len, _I32, (B,), dev, "kv_len"),
+            _arg(out, _FLOATS, (B, T, H, shape.v_dim), dev, "out"),
             DSA_OUT_BF16 if out.dtype == torch.bfloat16 else DSA_OUT_F32,
-            _arg(lse, (torch.float32,), (B, T, H), dev, "lse"), _ptr(ws, None, "ws"), int(ws_bytes))
-    ctx, st = _on_device(q, stream, "q")
-    with ctx:
-        _raise(load_library().dsa_dense_attn_ex(ctypes.byref(shape), _lay(layout), *args, st))
+            _arg(lse, _F32, (B, T, H), dev, "lse"), _arg(ws, (torch.uint8,), None, dev, "ws"), ws_bytes)
 
 
 def dsa_check(stream=None):

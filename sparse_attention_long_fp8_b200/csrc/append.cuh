@@ -38,14 +38,11 @@ struct AppendParams {
   RopeAngles ak, ac;               // of the key, of the latent row
 };
 
+// Token `tok` by one warp; key, cs: its scratch (DI values, DI / 2 pairs).
 template <int DI, int DQK>
-__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_constant__ AppendParams p) {
+__device__ __forceinline__ void append_token(const AppendParams& p, long long tok, int lane, float* key,
+                                             float2* cs, const double* tk, const double* tc) {
   constexpr int PER = DI / 32;     // key values of a lane
-  __shared__ float skey[kAppendWarps][DI];
-  __shared__ float2 scs[kAppendWarps][DI / 2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const long long tok = static_cast<long long>(blockIdx.x) * kAppendWarps + warp;
-  if (tok >= p.tokens) return;     // no barrier below spans warps
   const int b = static_cast<int>(tok / p.n_q), i = static_cast<int>(tok - static_cast<long long>(b) * p.n_q);
   if (p.n_new && i >= p.n_new[b]) return;
   const int pos = (p.q_pos0 ? p.q_pos0[b] : 0) + i;
@@ -90,7 +87,7 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
   }
   for (int j = lane; j < p.ac.pairs; j += 32) {
     const int ea = c0 + (p.ac.half ? j : 2 * j), eb = p.ac.half ? ea + p.ac.pairs : ea + 1;
-    const float2 t = rope_cos_sin(p.ac.turns[j], pos, p.ac.amplitude);
+    const float2 t = rope_cos_sin(tc[j], pos, p.ac.amplitude);
     const float x = __bfloat162float(cr[ea]), y = __bfloat162float(cr[eb]);
     kvr[ea] = __float2bfloat16_rn(x * t.x - y * t.y);
     kvr[eb] = __float2bfloat16_rn(x * t.y + y * t.x);
@@ -117,10 +114,10 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
   for (int j = 0; j < PER; ++j) {
     const int e = lane * PER + j;
     v[j] = fmaf(v[j] * rstd, p.w ? p.w[e] : 1.f, p.b ? p.b[e] : 0.f);
-    skey[warp][e] = v[j];
+    key[e] = v[j];
   }
   for (int j = lane; j < p.ak.pairs; j += 32)
-    scs[warp][j] = rope_cos_sin(p.ak.turns[j], pos, p.ak.amplitude);
+    cs[j] = rope_cos_sin(tk[j], pos, p.ak.amplitude);
   __syncwarp();
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
@@ -129,8 +126,8 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
     const bool second = p.ak.half ? e >= p.ak.pairs : (e & 1);
     const int pr = p.ak.half ? (second ? e - p.ak.pairs : e) : e >> 1;
     const int other = p.ak.begin + (p.ak.half ? (second ? e - p.ak.pairs : e + p.ak.pairs) : e ^ 1);
-    const float2 t = scs[warp][pr];
-    const float o = skey[warp][other];
+    const float2 t = cs[pr];
+    const float o = key[other];
     v[j] = second ? o * t.y + v[j] * t.x : v[j] * t.x - o * t.y;
   }
   float amax = 0.f;
@@ -149,6 +146,24 @@ __global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_
   if constexpr (PER == 4) *reinterpret_cast<uint32_t*>(codes) = packed;
   else *codes = static_cast<uint8_t>(packed);
   if (lane == 0) p.k_scale[at] = scale;
+}
+
+template <int DI, int DQK>
+__global__ void __launch_bounds__(32 * kAppendWarps) append_kernel(const __grid_constant__ AppendParams p) {
+  __shared__ float skey[kAppendWarps][DI];
+  __shared__ float2 scs[kAppendWarps][DI / 2];
+  __shared__ double tk[kRopeMaxPairs], tc[kRopeMaxPairs];    // turns per position
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j = threadIdx.x; j < p.ak.pairs; j += 32 * kAppendWarps) tk[j] = p.ak.turns[j];
+  for (int j = threadIdx.x; j < p.ac.pairs; j += 32 * kAppendWarps) tc[j] = p.ac.turns[j];
+  __syncthreads();
+  // no barrier below spans warps
+  for (long long tok = static_cast<long long>(blockIdx.x) * kAppendWarps + warp; tok < p.tokens;
+       tok += static_cast<long long>(gridDim.x) * kAppendWarps) 
+{
+    append_token<DI, DQK>(p, tok, lane, skey[warp], scs[warp], tk, tc);
+    __syncwarp();                  // the scratch has been read
+  }
 }
 
 }  // namespace dsa

@@ -62,6 +62,7 @@ struct DenseParams {
 
 struct DenseTile : VhTile {
   static constexpr int THREADS = 384;           // TMA 0, S MMA 1, PV MMA 2, softmax 4-11
+  static constexpr int AHEAD = 5;               // blocks whose lines are on their way into L2
   static constexpr int SM0 = 4;                 // first softmax warp
   static constexpr int NUM_BARS = 4 * STAGES + 8;
   static constexpr int OFF_SCAN = OFF_BAR + NUM_BARS * 8;      // [12] sums, then the start
@@ -234,6 +235,10 @@ __global__ void __launch_bounds__(384, 1)
         const int y = at;
         if (i + 1 < w.n) at = locate(blk + 1);   // one block ahead
         uint8_t* dst = c_smem + st * T::STAGE_BYTES;
+        if (i + T::AHEAD < w.n) {
+          const int yp = locate(blk + T::AHEAD);
+          if (lane < T::NDB && (lane & 1) == vh) tma_prefetch_2d(&tmap_kv, lane * 64, yp);
+        }
         ok = mbar_wait(&cx_empty[st], ph);
         if (!ok) break;
         if (valid >= NK) {
@@ -648,63 +653,110 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // Joins the partials of the rows that more than one share holds, in key order,
-// and writes the rows that see no key (out = 0, LSE = -inf). One CTA per (row,
-// head), four value dims per thread. The shares are derived as the attention
-// kernel derives them.
-__global__ void __launch_bounds__(128) dense_combine_kernel(const DenseParams p) {
-  __shared__ long long scan[4];
-  const int row = blockIdx.x, h = blockIdx.y;
-  long long all = 0, ahead = 0;
-  for (int r = threadIdx.x; r < p.rows; r += 128) {
+// and writes the rows that see no key (out = 0, LSE = -inf). G warps per (row,
+// head) take every G-th partial, a lane 16 of the 512 value dims; their sums
+// meet in shared memory. The shares are derived as the attention kernel derives
+// them. Few rows may have a partial from every pair (one long sequence: 74 of
+// them), so they get more warps: 36 -> 8 us with G = 8 against one thread
+// walking all partials.
+template <int G>
+__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseParams p) {
+  constexpr int HEADS = 8 / G;                   // heads per CTA
+  __shared__ longlong2 scan[8];
+  __shared__ float4 acc_s[G > 1 ? 8 : 1][4][32];
+  __shared__ float sum_s[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x;
+  const int h = blockIdx.y * HEADS + warp / G, sub = warp % G;
+  long long total = 0, first = 0;                // blocks of all rows, of the rows ahead
+  for (int r = threadIdx.x; r < p.rows; r += 256) {
     const int nb = p.blocks(r);
-    all += nb;
-    if (r < row) ahead += nb;
+    total += nb;
+    if (r < row) first += nb;
   }
-  const long long total = dense_block_sum<4>(all, scan);
-  const long long first = dense_block_sum<4>(ahead, scan);      // the row's first block
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    first += __shfl_xor_sync(0xffffffffu, first, o);
+  }
+  if (lane == 0) scan[warp] = make_longlong2(total, first);
+  __syncthreads();
+  total = first = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    total += scan[i].x;
+    first += scan[i].y;
+  }
   const int nb = p.blocks(row);
-  const size_t o = (static_cast<size_t>(row) * p.H + h) * 512 + threadIdx.x * 4;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float lse = -INFINITY;
-  if (nb > 0) {
-    const long long share = p.share(total);
-    const int p0 = static_cast<int>(first / share);
-    const int p1 = static_cast<int>((first + nb - 1) / share);
-    griddep_wait();                              // every CTA: this grid ends after the attention
-    if (p0 == p1) return;                        // written by the attention kernel
-    // the row begins in share p0 (slot 2 p0 + 1) and is what the others begin inside of
-    auto slot = [&](int q) { return static_cast<size_t>(q == p0 ? 2 * q + 1 : 2 * q); };
-    float m = -INFINITY;
-    for (int q = p0; q <= p1; ++q) m = fmaxf(m, p.part_lse[slot(q) * p.H + h]);
-    float sum = 0.f;
-#pragma unroll 4
-    for (int q = p0; q <= p1; ++q) {
-      const size_t at = slot(q) * p.H + h;
+  const long long share = p.share(total);
+  const int p0 = static_cast<int>(first / share);
+  const int np = nb > 0 ? static_cast<int>((first + nb - 1) / share) - p0 + 1 : 0;
+  griddep_wait();                                // every CTA: this grid ends after the attention
+  if (np == 1) return;                           // written by the attention kernel
+  // the row begins in share p0 (slot 2 p0 + 1); the others begin inside of it
+  auto slot = [&](int i) {
+    return (static_cast<size_t>(2 * (p0 + i)) + (i == 0 ? 1 : 0)) * p.H + h;
+  };
+  const bool there = h < p.H;
+  float m = -INFINITY;
+  if (there)
+    for (int i = lane; i < np; i += 32) m = fmaxf(m, p.part_lse[slot(i)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  float4 acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f;
+  if (there) {
+#pragma unroll 2
+    for (int i = sub; i < np; i += G) {
+      const size_t at = slot(i);
       const float ls = p.part_lse[at];
       const float wgt = ls == -INFINITY ? 0.f : __expf(ls - m);
-      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * 512 + threadIdx.x * 4);
       sum += wgt;
-      acc.x = fmaf(wgt, v.x, acc.x);
-      acc.y = fmaf(wgt, v.y, acc.y);
-      acc.z = fmaf(wgt, v.z, acc.z);
-      acc.w = fmaf(wgt, v.w, acc.w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * 512 + j * 128 + lane * 4);
+        acc[j].x = fmaf(wgt, v.x, acc[j].x);
+        acc[j].y = fmaf(wgt, v.y, acc[j].y);
+        acc[j].z = fmaf(wgt, v.z, acc[j].z);
+        acc[j].w = fmaf(wgt, v.w, acc[j].w);
+      }
     }
-    if (sum != 0.f) {                            // true for NaN
-      const float inv = 1.0f / sum;
-      acc.x *= inv; acc.y *= inv; acc.z *= inv; acc.w *= inv;
-      lse = m + logf(sum);
+  }
+  if constexpr (G > 1) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc_s[warp][j][lane] = acc[j];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+      sum += sum_s[warp + k];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float4 v = acc_s[warp + k][j][lane];
+        acc[j].x += v.x; acc[j].y += v.y; acc[j].z += v.z; acc[j].w += v.w;
+      }
     }
-  } else {
-    griddep_wait();                              // an earlier reader of out may still run
   }
-  if (p.out_bf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), b = __floats2bfloat162_rn(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + o) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + o) = acc;
+  if (!there) return;
+  const float inv = sum != 0.f ? 1.0f / sum : 0.f;     // NaN goes through
+  const size_t o = (static_cast<size_t>(row) * p.H + h) * 512;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 v = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
+    const size_t at = o + j * 128 + lane * 4;
+    if (p.out_bf16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+    }
   }
-  if (threadIdx.x == 0 && p.lse) p.lse[static_cast<size_t>(row) * p.H + h] = lse;
+  if (lane == 0 && p.lse)
+    p.lse[static_cast<size_t>(row) * p.H + h] = sum != 0.f ? m + logf(sum) : -INFINITY;
 }
 
 }  // namespace dsa

@@ -799,7 +799,12 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
     return st;
   dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, to, tp, p);
   DSA_CUDA_TRY(cudaGetLastError(), "dense attention launch");
-  DSA_CUDA_TRY(launch_dependent(dsa::dense_combine_kernel, dim3(p.rows, p.H), dim3(128), 0, stream, p),
+  // the fewer rows, the more partials a row may have
+  const int g = p.rows <= 8 ? 8 : (p.rows <= 32 ? 4 : 2);
+  const dim3 jgrid(p.rows, (p.H * g + 7) / 8);
+  DSA_CUDA_TRY(g == 8   ? launch_dependent(dsa::dense_combine_kernel<8>, jgrid, dim3(256), 0, stream, p)
+               : g == 4 ? launch_dependent(dsa::dense_combine_kernel<4>, jgrid, dim3(256), 0, stream, p)
+                        : launch_dependent(dsa::dense_combine_kernel<2>, jgrid, dim3(256), 0, stream, p),
                "dense attention join launch");
   return DSA_OK;
 }
@@ -899,46 +904,69 @@ NormPick norm_pick(int dim) {
 int norm_groups(int tpr) { return tpr <= 32 ? 256 / tpr : 1; }
 
 // CTAs of the two kernels: they walk the rows, so as many as are resident
-// (about 1024 threads per SM for the gradient), fewer when there are few rows.
-unsigned norm_grid(int64_t rows, int dim, int threads_per_sm) {
+// (the kernels' register bounds: MIN_CTAS), fewer when there are few rows.
+unsigned norm_grid(int64_t rows, int dim, bool gradient) {
   const NormPick k = norm_pick(dim);
-  const int threads = k.tpr <= 32 ? 256 : k.tpr;
   const int64_t need = (rows + norm_groups(k.tpr) - 1) / norm_groups(k.tpr);
-  const int64_t most = static_cast<int64_t>(num_sms()) * std::max(1, threads_per_sm / threads);
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min(need, most)));
+  int per_sm;
+  if (gradient) per_sm = k.tpr <= 32 ? 2 : (k.tpr == 128 ? 4 : 1);
+  else per_sm = k.tpr <= 32 ? 4 : (k.tpr == 128 ? 6 : (k.tpr == 512 ? 2 : 1));
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * per_sm)));
 }
 
+// The element types are compiled in where rows are narrow (dim <= 256: more
+// rows fit the registers); elsewhere the kernel is told at run time.
+template <bool VEC, int TPR, int NV>
+void launch_norm_t(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
+  constexpr int threads = dsa::norm_threads<TPR>();
+  if constexpr (VEC && TPR <= 32 && NV == 1) {
+    if (p.x_bf16) dsa::norm_kernel<VEC, TPR, NV, dsa::kRowBf16><<<grid, threads, 0, st>>>(p);
+    else dsa::norm_kernel<VEC, TPR, NV, dsa::kRowF32><<<grid, threads, 0, st>>>(p);
+  } else {
+    dsa::norm_kernel<VEC, TPR, NV, dsa::kRowAny><<<grid, threads, 0, st>>>(p);
+  }
+}
+template <bool VEC, int TPR, int NV>
+void launch_norm_bwd_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
+  using namespace dsa;
+  constexpr int threads = norm_threads<TPR>();
+  if constexpr (VEC && TPR <= 32 && NV == 1) {
+    if (p.x_bf16 && p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowBf16><<<grid, threads, 0, st>>>(p);
+    else if (p.x_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowF32><<<grid, threads, 0, st>>>(p);
+    else if (p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowF32, kRowBf16><<<grid, threads, 0, st>>>(p);
+    else norm_bwd_kernel<VEC, TPR, NV, kRowF32, kRowF32><<<grid, threads, 0, st>>>(p);
+  } else {
+    norm_bwd_kernel<VEC, TPR, NV, kRowAny, kRowAny><<<grid, threads, 0, st>>>(p);
+  }
+}
 template <bool VEC>
 void launch_norm(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
   const NormPick k = norm_pick(p.dim);
-  const int threads = k.tpr <= 32 ? 256 : k.tpr;
   switch (k.tpr * 4 + k.nv) {
-    case 16 * 4 + 1: dsa::norm_kernel<VEC, 16, 1><<<grid, threads, 0, st>>>(p); break;
-    case 32 * 4 + 1: dsa::norm_kernel<VEC, 32, 1><<<grid, threads, 0, st>>>(p); break;
-    case 32 * 4 + 2: dsa::norm_kernel<VEC, 32, 2><<<grid, threads, 0, st>>>(p); break;
-    case 128 * 4 + 1: dsa::norm_kernel<VEC, 128, 1><<<grid, threads, 0, st>>>(p); break;
-    case 128 * 4 + 2: dsa::norm_kernel<VEC, 128, 2><<<grid, threads, 0, st>>>(p); break;
-    case 512 * 4 + 1: dsa::norm_kernel<VEC, 512, 1><<<grid, threads, 0, st>>>(p); break;
-    case 512 * 4 + 2: dsa::norm_kernel<VEC, 512, 2><<<grid, threads, 0, st>>>(p); break;
-    default: dsa::norm_kernel<VEC, 1024, 2><<<grid, threads, 0, st>>>(p); break;
+    case 16 * 4 + 1: launch_norm_t<VEC, 16, 1>(p, grid, st); break;
+    case 32 * 4 + 1: launch_norm_t<VEC, 32, 1>(p, grid, st); break;
+    case 32 * 4 + 2: launch_norm_t<VEC, 32, 2>(p, grid, st); break;
+    case 128 * 4 + 1: launch_norm_t<VEC, 128, 1>(p, grid, st); break;
+    case 128 * 4 + 2: launch_norm_t<VEC, 128, 2>(p, grid, st); break;
+    case 512 * 4 + 1: launch_norm_t<VEC, 512, 1>(p, grid, st); break;
+    case 512 * 4 + 2: launch_norm_t<VEC, 512, 2>(p, grid, st); break;
+    default: launch_norm_t<VEC, 1024, 2>(p, grid, st); break;
   }
 }
 template <bool VEC>
 void launch_norm_bwd(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
   const NormPick k = norm_pick(p.dim);
-  const int threads = k.tpr <= 32 ? 256 : k.tpr;
   switch (k.tpr * 4 + k.nv) {
-    case 16 * 4 + 1: dsa::norm_bwd_kernel<VEC, 16, 1><<<grid, threads, 0, st>>>(p); break;
-    case 32 * 4 + 1: dsa::norm_bwd_kernel<VEC, 32, 1><<<grid, threads, 0, st>>>(p); break;
-    case 32 * 4 + 2: dsa::norm_bwd_kernel<VEC, 32, 2><<<grid, threads, 0, st>>>(p); break;
-    case 128 * 4 + 1: dsa::norm_bwd_kernel<VEC, 128, 1><<<grid, threads, 0, st>>>(p); break;
-    case 128 * 4 + 2: dsa::norm_bwd_kernel<VEC, 128, 2><<<grid, threads, 0, st>>>(p); break;
-    case 512 * 4 + 1: dsa::norm_bwd_kernel<VEC, 512, 1><<<grid, threads, 0, st>>>(p); break;
-    case 512 * 4 + 2: dsa::norm_bwd_kernel<VEC, 512, 2><<<grid, threads, 0, st>>>(p); break;
-    default: dsa::norm_bwd_kernel<VEC, 1024, 2><<<grid, threads, 0, st>>>(p); break;
+    case 16 * 4 + 1: launch_norm_bwd_t<VEC, 16, 1>(p, grid, st); break;
+    case 32 * 4 + 1: launch_norm_bwd_t<VEC, 32, 1>(p, grid, st); break;
+    case 32 * 4 + 2: launch_norm_bwd_t<VEC, 32, 2>(p, grid, st); break;
+    case 128 * 4 + 1: launch_norm_bwd_t<VEC, 128, 1>(p, grid, st); break;
+    case 128 * 4 + 2: launch_norm_bwd_t<VEC, 128, 2>(p, grid, st); break;
+    case 512 * 4 + 1: launch_norm_bwd_t<VEC, 512, 1>(p, grid, st); break;
+    case 512 * 4 + 2: launch_norm_bwd_t<VEC, 512, 2>(p, grid, st); break;
+    default: launch_norm_bwd_t<VEC, 1024, 2>(p, grid, st); break;
   }
 }
-constexpr int kNormBwdThreadsPerSm = 1024;
 
 dsa_status check_norm_shape(int64_t rows, int32_t dim) {
   if (rows < 0 || rows > (1ll << 40))
@@ -1598,8 +1626,8 @@ dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dty
   p.x_bf16 = x_dtype == DSA_BF16;
   p.y_bf16 = y_dtype == DSA_BF16;
   p.eps = eps;
-  const unsigned grid = norm_grid(rows, dim, 2048);
-  if (dim % 8 == 0 && norm_vec(tx) && norm_vec(ty)) launch_norm<true>(p, grid, static_cast<cudaStream_t>(stream));
+  const unsigned grid = norm_grid(rows, dim, false);
+  if (dim % 8 == 0 && norm_vec(tx) && norm_vec(ty) && aligned(weight, 16) && aligned(bias, 16)) launch_norm<true>(p, grid, static_cast<cudaStream_t>(stream));
   else launch_norm<false>(p, grid, static_cast<cudaStream_t>(stream));
   DSA_CUDA_TRY(cudaGetLastError(), "layer norm launch");
   return DSA_OK;
@@ -1610,7 +1638,7 @@ dsa_status dsa_layernorm_bwd_workspace(int64_t rows, int32_t dim, size_t* bytes)
   *bytes = 0;
   if (dsa_status st = check_norm_shape(rows, dim)) return st;
   if (rows > 0)
-    *bytes = static_cast<size_t>(norm_grid(rows, dim, kNormBwdThreadsPerSm)) * 2 * dim * sizeof(float);
+    *bytes = static_cast<size_t>(norm_grid(rows, dim, true)) * 2 * dim * sizeof(float);
   return DSA_OK;
 }
 
@@ -1632,7 +1660,7 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
       !aligned(dbias, 4))
     return fail(DSA_ERR_INVALID_ARG, "dsa_layernorm_bwd: fp32 arrays must be 4-byte aligned");
   const bool sums = dweight || dbias;
-  const unsigned grid = norm_grid(rows, dim, kNormBwdThreadsPerSm);
+  const unsigned grid = norm_grid(rows, dim, true);
   const size_t need = sums && rows > 0 ? static_cast<size_t>(grid) * 2 * dim * sizeof(float) : 0;
   if (need > 0) {
     if (!ws || ws_bytes < need)
@@ -1662,7 +1690,7 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
     p.dy_bf16 = dy_dtype == DSA_BF16;
     p.x_bf16 = x_dtype == DSA_BF16;
     p.dx_bf16 = dx_dtype == DSA_BF16;
-    if (dim % 8 == 0 && norm_vec(tdy) && norm_vec(tx) && norm_vec(tdx)) launch_norm_bwd<true>(p, grid, st_);
+    if (dim % 8 == 0 && norm_vec(tdy) && norm_vec(tx) && norm_vec(tdx) && aligned(weight, 16)) launch_norm_bwd<true>(p, grid, st_);
     else launch_norm_bwd<false>(p, grid, st_);
     DSA_CUDA_TRY(cudaGetLastError(), "layer norm gradient launch");
   }
@@ -1726,7 +1754,8 @@ dsa_status dsa_cache_append(const dsa_shape* s, const dsa_layout* layout, const 
   p.eps = eps;
   p.ak = rope_angles(idx_rope);
   p.ac = rope_angles(kv_rope);
-  const unsigned grid = static_cast<unsigned>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps);
+  const unsigned grid = static_cast<unsigned>(
+      std::min<int64_t>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps, 12ll * num_sms()));
   constexpr int threads = 32 * dsa::kAppendWarps;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   if (s->idx_dim == 128) {

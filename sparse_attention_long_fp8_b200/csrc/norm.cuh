@@ -8,8 +8,7 @@
 // Bound: HBM, each row read once and written once. A row stays in registers
 // between its passes (two passes for the variance: sum of squares minus
 // squared mean would cancel in fp32 when |mean| >> sigma). TPR threads share a
-// row and hold 8 NV elements each; with NV = 1 the next row's loads are issued
-// before this row is reduced (wider rows have more CTAs' loads in flight). All arithmetic is fp32; bf16 only at loads and stores.
+// row and hold 8 NV elements each. All arithmetic is fp32; bf16 only at loads and stores.
 //
 // The weight's gradient: a thread keeps the sums of its columns over all the
 // rows its CTA walks, the CTA writes one partial row, and a second kernel adds
@@ -50,33 +49,38 @@ struct NormBwdParams {
   int dy_bf16, x_bf16, dx_bf16;
 };
 
+// Element types of a row tensor as a template argument; kAny: told at run time.
+enum { kRowF32 = 0, kRowBf16 = 1, kRowAny = 2 };
+
 // One thread's elements of a row as loaded: 8 NV of them in chunks of 8
 // (VEC, 16-byte loads) or one by one, TPR apart.
-template <bool VEC, int TPR, int NV>
+template <bool VEC, int TPR, int NV, int TYPE>
 struct NormRow {
   static constexpr int EPT = 8 * NV;
-  uint32_t w[EPT];                 // fp32 bits, or for VEC bf16 pairs in the first half
+  static constexpr int PER = VEC && TYPE == kRowBf16 ? 4 : 8;    // words per chunk
+  uint32_t w[PER * NV];            // fp32 bits, or for VEC bf16 pairs in a chunk's first 4
 
   __device__ __forceinline__ static int elem(int lane, int j) {
     return VEC ? ((j >> 3) * TPR + lane) * 8 + (j & 7) : j * TPR + lane;
   }
-  __device__ __forceinline__ void load(const void* base, long long off, int bf16, int lane, int dim) {
+  __device__ __forceinline__ static bool is_bf16(int flag) {
+    return TYPE == kRowAny ? flag != 0 : TYPE == kRowBf16;
+  }
+  __device__ __forceinline__ void load(const void* base, long long off, int flag, int lane, int dim) {
     if constexpr (VEC) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         const int e = elem(lane, 8 * v);
-        if (bf16) {
-          uint4 u = make_uint4(0, 0, 0, 0);
+        uint4 u = make_uint4(0, 0, 0, 0), t = u;
+        if (is_bf16(flag)) {
           if (e < dim) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off + e);
-          w[8 * v] = u.x; w[8 * v + 1] = u.y; w[8 * v + 2] = u.z; w[8 * v + 3] = u.w;
-        } else {
-          uint4 u = make_uint4(0, 0, 0, 0), t = u;
-          if (e < dim) {
-            const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + off + e);
-            u = s[0];
-            t = s[1];
-          }
-          w[8 * v] = u.x; w[8 * v + 1] = u.y; w[8 * v + 2] = u.z; w[8 * v + 3] = u.w;
+        } else if (e < dim) {
+          const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + off + e);
+          u = s[0];
+          t = s[1];
+        }
+        w[PER * v] = u.x; w[PER * v + 1] = u.y; w[PER * v + 2] = u.z; w[PER * v + 3] = u.w;
+        if constexpr (PER == 8) {
           w[8 * v + 4] = t.x; w[8 * v + 5] = t.y; w[8 * v + 6] = t.z; w[8 * v + 7] = t.w;
         }
       }
@@ -86,63 +90,84 @@ struct NormRow {
         const int e = elem(lane, j);
         w[j] = 0u;
         if (e < dim)
-          w[j] = bf16 ? static_cast<uint32_t>(static_cast<const uint16_t*>(base)[off + e]) << 16
-                      : __float_as_uint(static_cast<const float*>(base)[off + e]);
+          w[j] = is_bf16(flag) ? static_cast<uint32_t>(static_cast<const uint16_t*>(base)[off + e]) << 16
+                               : __float_as_uint(static_cast<const float*>(base)[off + e]);
       }
     }
   }
   // Elements past dim read as 0.
-  __device__ __forceinline__ void get(float (&f)[EPT], int bf16) const {
-    if (VEC && bf16) {
+  __device__ __forceinline__ void get(float (&f)[EPT], int flag) const {
+    if (VEC && is_bf16(flag)) {
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
-        const uint32_t u = w[(j & ~7) + ((j & 7) >> 1)];
+        const uint32_t u = w[(j >> 3) * PER + ((j & 7) >> 1)];
         f[j] = __uint_as_float((j & 1) ? (u & 0xffff0000u) : (u << 16));
       }
-    } else {
+    } else if constexpr (!VEC || TYPE != kRowBf16) {
 #pragma unroll
       for (int j = 0; j < EPT; ++j) f[j] = __uint_as_float(w[j]);
     }
   }
-  __device__ __forceinline__ static void store(void* base, long long off, int bf16, int lane, int dim,
-                                               const float (&f)[EPT]) {
-    if constexpr (VEC) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int e = elem(lane, 8 * v);
-        if (e >= dim) continue;
-        if (bf16) {
-          uint32_t u[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * v + 2 * j], f[8 * v + 2 * j + 1]);
-            u[j] = *reinterpret_cast<const uint32_t*>(&h);
-          }
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off + e) =
-              make_uint4(u[0], u[1], u[2], u[3]);
-        } else {
-          float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + off + e);
-          d[0] = make_float4(f[8 * v], f[8 * v + 1], f[8 * v + 2], f[8 * v + 3]);
-          d[1] = make_float4(f[8 * v + 4], f[8 * v + 5], f[8 * v + 6], f[8 * v + 7]);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPT; ++j) {
-        const int e = elem(lane, j);
-        if (e >= dim) continue;
-        if (bf16) static_cast<__nv_bfloat16*>(base)[off + e] = __float2bfloat16_rn(f[j]);
-        else static_cast<float*>(base)[off + e] = f[j];
-      }
-    }
-  }
 };
 
-// Sum of (a, b) over the TPR threads of a row. More than a warp: through
-// shared memory, `buf` alternating between two sets of slots so that one
-// barrier per sum suffices.
+// Stores one thread's elements of a row in the same arrangement.
+template <bool VEC, int TPR, int NV>
+__device__ __forceinline__ void norm_store(void* base, long long off, int bf16, int lane, int dim,
+                                           const float (&f)[8 * NV]) {
+  using Row = NormRow<VEC, TPR, NV, kRowAny>;
+  if constexpr (VEC) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = Row::elem(lane, 8 * v);
+      if (e >= dim) continue;
+      if (bf16) {
+        uint32_t u[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * v + 2 * j], f[8 * v + 2 * j + 1]);
+          u[j] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off + e) = make_uint4(u[0], u[1], u[2], u[3]);
+      } else {
+        float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + off + e);
+        d[0] = make_float4(f[8 * v], f[8 * v + 1], f[8 * v + 2], f[8 * v + 3]);
+        d[1] = make_float4(f[8 * v + 4], f[8 * v + 5], f[8 * v + 6], f[8 * v + 7]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8 * NV; ++j) {
+      const int e = Row::elem(lane, j);
+      if (e >= dim) continue;
+      if (bf16) static_cast<__nv_bfloat16*>(base)[off + e] = __float2bfloat16_rn(f[j]);
+      else static_cast<float*>(base)[off + e] = f[j];
+    }
+  }
+}
+
+// One thread's fp32 weights in a row's arrangement: `fill` where there are none.
+template <bool VEC, int TPR, int NV>
+__device__ __forceinline__ void norm_weights(const float* w, float fill, int lane, int dim,
+                                             float (&f)[8 * NV]) {
+  using Row = NormRow<VEC, TPR, NV, kRowAny>;
+#pragma unroll
+  for (int j = 0; j < 8 * NV; j += VEC ? 4 : 1) {
+    const int e = Row::elem(lane, j);
+    if constexpr (VEC) {
+      float4 v = make_float4(fill, fill, fill, fill);
+      if (w && e < dim) v = __ldg(reinterpret_cast<const float4*>(w + e));
+      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+    } else {
+      f[j] = w && e < dim ? __ldg(w + e) : fill;
+    }
+  }
+}
+
+// Sums over the TPR threads of a row. More than a warp: through shared memory,
+// `buf` alternating between two sets of slots so that one barrier per sum
+// suffices.
 template <int TPR>
-__device__ __forceinline__ float2 norm_sum(float a, float b, float2* slots, int& buf) {
+__device__ __forceinline__ float2 norm_sum2(float a, float b, float2* slots, int& buf) {
 #pragma unroll
   for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     a += __shfl_xor_sync(0xffffffffu, a, o);
@@ -164,16 +189,44 @@ __device__ __forceinline__ float2 norm_sum(float a, float b, float2* slots, int&
   }
   return make_float2(a, b);
 }
+template <int TPR>
+__device__ __forceinline__ float norm_sum(float a, float2* slots, int& buf) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  if constexpr (TPR > 32) {
+    constexpr int W = TPR / 32;
+    float2* s = slots + buf * W;
+    buf ^= 1;
+    if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5].x = a;
+    __syncthreads();
+    a = 0.f;
+#pragma unroll
+    for (int i = 0; i < W; ++i) a += s[i].x;
+  }
+  return a;
+}
 
 // Threads per CTA: rows of up to a warp's threads share one.
 template <int TPR>
 constexpr int norm_threads() { return TPR <= 32 ? 256 : TPR; }
 
-template <bool VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>()) norm_kernel(const NormParams p) {
-  using Row = NormRow<VEC, TPR, NV>;
+// How a group keeps bytes in flight: narrow rows are loaded U at a time, wide
+// ones one row ahead (PRE); a row of two chunks per thread leaves no registers
+// for either and relies on the other CTAs. MIN_CTAS per SM bounds the registers.
+template <int TPR, int NV, int TYPE>
+struct NormFlow {
+  static constexpr int U = TPR <= 32 && NV == 1 ? (TYPE == kRowBf16 ? 4 : 2) : 1;
+  static constexpr bool PRE = U == 1 && NV == 1;
+  static constexpr bool KEEP = NV == 1;                  // weights stay in registers
+  static constexpr int MIN_CTAS = TPR <= 32 ? 4 : (TPR == 128 ? 6 : (TPR == 512 ? 2 : 1));
+};
+
+template <bool VEC, int TPR, int NV, int TYPE>
+__global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::MIN_CTAS)
+    norm_kernel(const NormParams p) {
+  using Row = NormRow<VEC, TPR, NV, TYPE>;
+  using F = NormFlow<TPR, NV, TYPE>;
   constexpr int EPT = Row::EPT, GROUPS = norm_threads<TPR>() / TPR;
-  constexpr bool PRE = NV == 1;    // the next row and the weights in registers
   __shared__ float2 slots[TPR > 32 ? 2 * TPR / 32 : 1];
   int buf = 0;
   const int lane = threadIdx.x % TPR;
@@ -182,77 +235,87 @@ __global__ void __launch_bounds__(norm_threads<TPR>()) norm_kernel(const NormPar
   // past the last row loads nothing and stores nothing.
   const long long base = static_cast<long long>(blockIdx.x) * GROUPS;
   const int g = threadIdx.x / TPR;
-  Row cur, next;
-  if (PRE && base + g < p.rows) cur.load(p.x, (base + g) * p.xs, p.x_bf16, lane, p.dim);
-  auto weight = [&](int j) {
-    const int e = Row::elem(lane, j);
-    return p.w && e < p.dim ? __ldg(p.w + e) : 1.f;
-  };
-  auto bias = [&](int j) {
-    const int e = Row::elem(lane, j);
-    return p.b && e < p.dim ? __ldg(p.b + e) : 0.f;
-  };
-  float w[PRE ? EPT : 1], b[PRE ? EPT : 1];
-  if constexpr (PRE) {
-#pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-      w[j] = weight(j);
-      b[j] = bias(j);
-    }
+  Row raw[F::U], next;
+  if (F::PRE && base + g < p.rows) raw[0].load(p.x, (base + g) * p.xs, p.x_bf16, lane, p.dim);
+  float w[EPT], b[EPT];
+  if constexpr (F::KEEP) {
+    norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
+    norm_weights<VEC, TPR, NV>(p.b, 0.f, lane, p.dim, b);
   }
   const float inv = 1.0f / static_cast<float>(p.dim);
-  for (long long r0 = base; r0 < p.rows; r0 += step) {
-    const long long r = r0 + g;
-    if constexpr (PRE) {
-      if (r + step < p.rows) next.load(p.x, (r + step) * p.xs, p.x_bf16, lane, p.dim);
+  for (long long r0 = base; r0 < p.rows; r0 += step * F::U) {
+    if constexpr (F::PRE) {
+      if (r0 + g + step < p.rows) next.load(p.x, (r0 + g + step) * p.xs, p.x_bf16, lane, p.dim);
     } else {
-      if (r < p.rows) cur.load(p.x, r * p.xs, p.x_bf16, lane, p.dim);
-    }
-    float x[EPT];
-    cur.get(x, p.x_bf16);
-    float s = 0.f;
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) s += x[j];
-    const float mean = norm_sum<TPR>(s, 0.f, slots, buf).x * inv;
-    float q = 0.f;
-#pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-      x[j] -= mean;
-      if (Row::elem(lane, j) < p.dim) q = fmaf(x[j], x[j], q);
+      for (int u = 0; u < F::U; ++u) {
+        const long long r = r0 + g + u * step;
+        if (r < p.rows) raw[u].load(p.x, r * p.xs, p.x_bf16, lane, p.dim);
+      }
     }
-    const float var = norm_sum<TPR>(q, 0.f, slots, buf).x * inv;
-    const float rstd = 1.0f / sqrtf(var + p.eps);
-    if (r < p.rows) {
+#pragma unroll
+    for (int u = 0; u < F::U; ++u) {
+      if (u > 0 && r0 + u * step >= p.rows) break;       // the same in the whole CTA
+      const long long r = r0 + g + u * step;
+      float x[EPT];
+      raw[u].get(x, p.x_bf16);
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) s += x[j];
+      const float mean = norm_sum<TPR>(s, slots, buf) * inv;
+      float q = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
-        if constexpr (PRE) x[j] = fmaf(x[j] * rstd, w[j], b[j]);
-        else x[j] = fmaf(x[j] * rstd, weight(j), bias(j));
+        x[j] -= mean;
+        if (Row::elem(lane, j) < p.dim) q = fmaf(x[j], x[j], q);
       }
-      Row::store(p.y, r * p.ys, p.y_bf16, lane, p.dim, x);
-      if (lane == 0) {
-        if (p.mean) p.mean[r] = mean;
-        if (p.rstd) p.rstd[r] = rstd;
+      const float var = norm_sum<TPR>(q, slots, buf) * inv;
+      const float rstd = 1.0f / sqrtf(var + p.eps);
+      if (r < p.rows) {
+        if constexpr (!F::KEEP) {
+          norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
+          norm_weights<VEC, TPR, NV>(p.b, 0.f, lane, p.dim, b);
+        }
+#pragma unroll
+        for (int j = 0; j < EPT; ++j) x[j] = fmaf(x[j] * rstd, w[j], b[j]);
+        norm_store<VEC, TPR, NV>(p.y, r * p.ys, p.y_bf16, lane, p.dim, x);
+        if (lane == 0) {
+          if (p.mean) p.mean[r] = mean;
+          if (p.rstd) p.rstd[r] = rstd;
+        }
       }
     }
-    if constexpr (PRE) cur = next;
+    if constexpr (F::PRE) raw[0] = next;
   }
 }
 
-template <bool VEC, int TPR, int NV>
-__global__ void __launch_bounds__(norm_threads<TPR>(), 1) norm_bwd_kernel(const NormBwdParams p) {
-  using Row = NormRow<VEC, TPR, NV>;
-  constexpr int EPT = Row::EPT, THREADS = norm_threads<TPR>(), GROUPS = THREADS / TPR;
+// The same for the gradient, which loads two rows and keeps column sums.
+template <int TPR, int NV>
+struct NormBwdFlow {
+  static constexpr int U = TPR <= 32 && NV == 1 ? 2 : 1;
+  static constexpr bool PRE = U == 1 && NV == 1;
+  static constexpr bool KEEP = NV == 1;
+  static constexpr int MIN_CTAS = TPR <= 32 ? 2 : (TPR == 128 ? 4 : 1);
+};
+
+template <bool VEC, int TPR, int NV, int XT, int GT>
+__global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN_CTAS)
+    norm_bwd_kernel(const NormBwdParams p) {
+  using RowX = NormRow<VEC, TPR, NV, XT>;
+  using RowG = NormRow<VEC, TPR, NV, GT>;
+  using F = NormBwdFlow<TPR, NV>;
+  constexpr int EPT = RowX::EPT, THREADS = norm_threads<TPR>(), GROUPS = THREADS / TPR;
   constexpr int COLS = TPR * EPT;                       // columns a group covers, >= dim
-  constexpr bool PRE = NV == 1;    // the next row and the weights in registers
   __shared__ float2 slots[TPR > 32 ? 2 * TPR / 32 : 1];
   int buf = 0;
   const int lane = threadIdx.x % TPR;
   const long long step = static_cast<long long>(gridDim.x) * GROUPS;
   const long long base = static_cast<long long>(blockIdx.x) * GROUPS;
   const int g = threadIdx.x / TPR;
-  Row cx, cy, nx, ny;
-  float mean = 0.f, rstd = 0.f, nmean = 0.f, nrstd = 0.f;
-  auto fetch = [&](long long r, Row& rx, Row& ry, float& m, float& s) {
+  RowX cx[F::U], nx;
+  RowG cy[F::U], ny;
+  float mean[F::U], rstd[F::U], nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](long long r, RowX& rx, RowG& ry, float& m, float& s) {
     if (r < p.rows) {
       rx.load(p.x, r * p.xs, p.x_bf16, lane, p.dim);
       ry.load(p.dy, r * p.dys, p.dy_bf16, lane, p.dim);
@@ -260,52 +323,54 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), 1) norm_bwd_kernel(const 
       s = p.rstd[r];
     }
   };
-  if constexpr (PRE) fetch(base + g, cx, cy, mean, rstd);
-  auto weight = [&](int j) {
-    const int e = Row::elem(lane, j);
-    return p.w && e < p.dim ? __ldg(p.w + e) : 1.f;
-  };
-  float w[PRE ? EPT : 1], aw[EPT], ab[EPT];
+  if constexpr (F::PRE) fetch(base + g, cx[0], cy[0], mean[0], rstd[0]);
+  float w[EPT], aw[EPT], ab[EPT];
+  if constexpr (F::KEEP) norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
 #pragma unroll
-  for (int j = 0; j < EPT; ++j) {
-    if constexpr (PRE) w[j] = weight(j);
-    aw[j] = ab[j] = 0.f;
-  }
+  for (int j = 0; j < EPT; ++j) aw[j] = ab[j] = 0.f;
   const float inv = 1.0f / static_cast<float>(p.dim);
-  for (long long r0 = base; r0 < p.rows; r0 += step) {
-    const long long r = r0 + g;
-    const bool there = r < p.rows;
-    if constexpr (PRE) fetch(r + step, nx, ny, nmean, nrstd);
-    else fetch(r, cx, cy, mean, rstd);
-    float x[EPT], d[EPT];
-    cx.get(x, p.x_bf16);
-    cy.get(d, p.dy_bf16);
-    float sg = 0.f, sgx = 0.f;
+  for (long long r0 = base; r0 < p.rows; r0 += step * F::U) {
+    if constexpr (F::PRE) {
+      fetch(r0 + g + step, nx, ny, nmean, nrstd);
+    } else {
 #pragma unroll
-    for (int j = 0; j < EPT; ++j) {
-      // past the row's end d is 0 and so are its products
-      x[j] = Row::elem(lane, j) < p.dim ? (x[j] - mean) * rstd : 0.f;
-      if (there) {
-        aw[j] = fmaf(d[j], x[j], aw[j]);
-        ab[j] += d[j];
+      for (int u = 0; u < F::U; ++u) fetch(r0 + g + u * step, cx[u], cy[u], mean[u], rstd[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < F::U; ++u) {
+      if (u > 0 && r0 + u * step >= p.rows) break;       // the same in the whole CTA
+      const long long r = r0 + g + u * step;
+      const bool there = r < p.rows;
+      float x[EPT], d[EPT];
+      cx[u].get(x, p.x_bf16);
+      cy[u].get(d, p.dy_bf16);
+      if constexpr (!F::KEEP) norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
+      float sg = 0.f, sgx = 0.f;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j) {
+        // past the row's end d is 0 and so are its products
+        x[j] = RowX::elem(lane, j) < p.dim ? (x[j] - mean[u]) * rstd[u] : 0.f;
+        if (there) {
+          aw[j] = fmaf(d[j], x[j], aw[j]);
+          ab[j] += d[j];
+        }
+        d[j] *= w[j];
+        sg += d[j];
+        sgx = fmaf(d[j], x[j], sgx);
       }
-      if constexpr (PRE) d[j] *= w[j];
-      else d[j] *= weight(j);
-      sg += d[j];
-      sgx = fmaf(d[j], x[j], sgx);
-    }
-    const float2 s = norm_sum<TPR>(sg, sgx, slots, buf);
-    const float mg = s.x * inv, mgx = s.y * inv;
-    if (there) {
+      const float2 s = norm_sum2<TPR>(sg, sgx, slots, buf);
+      const float mg = s.x * inv, mgx = s.y * inv;
+      if (there) {
 #pragma unroll
-      for (int j = 0; j < EPT; ++j) d[j] = rstd * (d[j] - mg - x[j] * mgx);
-      Row::store(p.dx, r * p.dxs, p.dx_bf16, lane, p.dim, d);
+        for (int j = 0; j < EPT; ++j) d[j] = rstd[u] * (d[j] - mg - x[j] * mgx);
+        norm_store<VEC, TPR, NV>(p.dx, r * p.dxs, p.dx_bf16, lane, p.dim, d);
+      }
     }
-    if constexpr (PRE) {
-      cx = nx;
-      cy = ny;
-      mean = nmean;
-      rstd = nrstd;
+    if constexpr (F::PRE) {
+      cx[0] = nx;
+      cy[0] = ny;
+      mean[0] = nmean;
+      rstd[0] = nrstd;
     }
   }
   griddep_launch_dependents();
@@ -321,7 +386,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), 1) norm_bwd_kernel(const 
       for (int j = 0; j < EPT; ++j) {
         float v = k == 0 ? aw[j] : ab[j];
         if constexpr (TPR == 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
-        acc[threadIdx.x >> 5][Row::elem(lane, j)] = v;
+        acc[threadIdx.x >> 5][RowX::elem(lane, j)] = v;
       }
       __syncthreads();
       for (int e = threadIdx.x; e < p.dim; e += THREADS) {
@@ -335,7 +400,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), 1) norm_bwd_kernel(const 
   } else {
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
-      const int e = Row::elem(lane, j);
+      const int e = RowX::elem(lane, j);
       if (e < p.dim) {
         part[e] = aw[j];
         part[p.dim + e] = ab[j];
@@ -343,6 +408,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), 1) norm_bwd_kernel(const 
     }
   }
 }
+
+constexpr int kNormReduceUnroll = 10;   // partial rows a thread loads before it adds
 
 // dweight, dbias: the n partial rows [2][dim] added in a fixed order, 32
 // columns per CTA (of the 2 dim), 32 warps over the rows.
@@ -353,9 +420,16 @@ __global__ void __launch_bounds__(1024)
   const int c = blockIdx.x * 32 + lane;
   griddep_wait();
   float v = 0.f;
-  if (c < 2 * dim)
-#pragma unroll 4
-    for (int i = warp; i < n; i += 32) v += part[static_cast<size_t>(i) * 2 * dim + c];
+  for (int i0 = warp; i0 < n; i0 += 32 * kNormReduceUnroll) {
+    float t[kNormReduceUnroll];
+#pragma unroll
+    for (int k = 0; k < kNormReduceUnroll; ++k) {
+      const int i = i0 + 32 * k;
+      t[k] = i < n && c < 2 * dim ? part[static_cast<size_t>(i) * 2 * dim + c] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kNormReduceUnroll; ++k) v += t[k];
+  }
   acc[warp][lane] = v;
   __syncthreads();
   // column `warp` of the CTA: its 32 sums by a warp reduction

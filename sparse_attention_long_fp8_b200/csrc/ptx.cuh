@@ -158,6 +158,14 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// Brings the box of a 2D tiled load into L2.
+__device__ __forceinline__ void tma_prefetch_2d(const void* tmap, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y)
+               : "memory");
+}
+
 // 2D tiled store shared -> global (bulk group; x = innermost coordinate in
 // elements of the map, y = row). The source must be made visible to the
 // async proxy first (fence_proxy_async_smem by the writing threads, then a

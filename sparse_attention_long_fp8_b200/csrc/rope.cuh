@@ -14,7 +14,7 @@
 // Bound: HBM, one read and one write per element (in place: of the rotated
 // part only). Threads move 16-byte chunks when every address allows it (the
 // rotated part's halves and the strides are multiples of a chunk), single
-// elements otherwise; four rows are loaded before the first is turned.
+// elements otherwise; several rows are loaded before the first is turned.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -27,7 +27,9 @@ constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTableBytes = 32768;   // cos / sin of one CTA's tokens
 constexpr int kRopeMaxTokens = 512;      // tokens of one CTA
-constexpr int kRopeUnroll = 4;           // rows a thread loads before it turns any
+// Rows a thread loads before it turns any: 64 bytes of 16-byte chunks.
+template <int E, bool HALF>
+constexpr int rope_unroll() { return HALF && E > 1 ? 2 : 4; }
 
 // One rotation as the kernels take it (from dsa_rope_spec).
 struct RopeAngles {
@@ -96,7 +98,8 @@ struct alignas(E * sizeof(T)) RopeChunk {
 // of each half) or max(E / 2, 1) pairs (interleaved: one chunk, or two
 // neighbouring elements).
 template <class T, int E, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  constexpr int kUnroll = rope_unroll<E, HALF>();
   constexpr int HP = HALF ? E : (E > 1 ? E / 2 : 1);
   using Chunk = RopeChunk<T, E>;
   extern __shared__ float2 cs[];                       // [tokens][pairs]
@@ -144,13 +147,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int first = p.a.begin + (HALF ? item * E : 2 * item * HP);
     const int second = HALF ? first + P : first + 1;   // second: halves, or the scalar neighbour
     if (ry < lanes)
-      for (uint32_t r = row0 + ry; r < row1; r += lanes * kRopeUnroll) {
-        Chunk u[kRopeUnroll], w[kRopeUnroll];
-        int64_t oo[kRopeUnroll];
-        int tk[kRopeUnroll];
-        bool on[kRopeUnroll];
+      for (uint32_t r = row0 + ry; r < row1; r += lanes * kUnroll) {
+        Chunk u[kUnroll], w[kUnroll];
+        int64_t oo[kUnroll];
+        int tk[kUnroll];
+        bool on[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kRopeUnroll; ++k) {
+        for (int k = 0; k < kUnroll; ++k) {
           int64_t xo;
           on[k] = locate(r + k * lanes, xo, oo[k], tk[k]);
           if (on[k]) {
@@ -159,7 +162,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           }
         }
 #pragma unroll
-        for (int k = 0; k < kRopeUnroll; ++k) {
+        for (int k = 0; k < kUnroll; ++k) {
           if (!on[k]) continue;
           const float2* t = cs + tk[k] * P + item * HP;
 #pragma unroll
@@ -192,12 +195,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   for (int c = c0; c < chunks; c += 2 * wide) {
     const bool two = c + wide < chunks;
     const int e0 = at(c), e1 = at(two ? c + wide : c);
-    for (uint32_t r = row0 + ry; r < row1; r += lanes * kRopeUnroll) {
-      Chunk u[kRopeUnroll], w[kRopeUnroll];
-      int64_t oo[kRopeUnroll];
-      bool on[kRopeUnroll];
+    for (uint32_t r = row0 + ry; r < row1; r += lanes * kUnroll) {
+      Chunk u[kUnroll], w[kUnroll];
+      int64_t oo[kUnroll];
+      bool on[kUnroll];
 #pragma unroll
-      for (int k = 0; k < kRopeUnroll; ++k) {
+      for (int k = 0; k < kUnroll; ++k) {
         int64_t xo;
         int tk;
         on[k] = locate(r + k * lanes, xo, oo[k], tk);
@@ -207,7 +210,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         }
       }
 #pragma unroll
-      for (int k = 0; k < kRopeUnroll; ++k)
+      for (int k = 0; k < kUnroll; ++k)
         if (on[k]) {
           *reinterpret_cast<Chunk*>(out + oo[k] + e0) = u[k];
           if (two) *reinterpret_cast<Chunk*>(out + oo[k] + e1) = w[k];
