@@ -4,7 +4,7 @@
 // with the online softmax: running maximum m and sum l per head, O rescaled
 // when m grows.
 //
-// The work is cut along the caches. All query rows' 64-key blocks, row after
+// The work is cut along the caches. All query rows' 128-key blocks, row after
 // row, form one line; CTA pair p takes blocks [p share, (p + 1) share) of it,
 // whatever rows they belong to, so ragged lengths keep every SM equally busy
 // and one long sequence spreads over the whole GPU. A row that lies inside one
@@ -13,27 +13,46 @@
 // joins them in key order. Both kernels derive the cut from kv_len and the
 // positions on the device: the host never needs the lengths.
 //
-// Inside a pair, CTA v owns value half v: it forms the complete logits and
-// accumulates O for its 256 value dims (O 256 + S 64 + Q 192 TMEM columns =
-// 512; an O of 512 dims would leave no column for S). Warp roles: 0 loads key
-// blocks by TMA (nine 64-dim boxes per block, 128-byte swizzle, two stages,
-// each released in two parts); 1 issues S = Q K^T; 2 issues O += P V; 4-11 run
-// the softmax and the epilogue. S, P, Q and O are laid out as in
-// sparse_attn_vh.cuh.
+// The two CTAs of a pair (a cluster, two SMs) work on one block together with
+// tcgen05 over both (cta_group::2, M = 128 heads, 64 per CTA):
+//   S [128 x 128 keys] = Q K^T   each CTA holds Q of its 64 heads and loads 64
+//                                of the block's keys;
+//   O [128 x 512]     += P V     each CTA holds P of its heads and loads half
+//                                of the value dims of all 128 keys.
+// So every product is formed once, the softmax of a head stays inside one CTA,
+// and no partial result crosses SMs. (Two independent CTAs, one per value half,
+// form S twice: 2.9 K cycles per 64 keys, 0.69 ms for 64 sequences of 16-32 K
+// keys.) What bounds a block: shared memory, 147 KB of operand reads for S, 98
+// for PV, 138 KB of loads and 16 KB of P at 128 bytes a cycle = 3.1 K cycles,
+// then the tensor pipe with 2.2 K.
+//
+// TMEM per CTA (M = 128 over a pair keeps 64 rows per CTA: lanes 0-63 hold the
+// first half of the N columns of rows 0-63, lanes 64-127 the second half): O
+// 256 columns (two N = 256 accumulators), S 2 x 64.
+//
+// Key blocks stream through one ring of 16 KB entries, one TMA copy each, in the
+// order the MMAs read them: S(i + 1) as five entries (64 keys x 128 dims, the
+// last one 64), then V(i) as four (64 keys x 128 dims). V is loaded a second time
+// (from L2) rather than kept from S: held back until its P exists it would
+// leave no room to load ahead.
 //
 // Rows behind a sequence's last key may hold anything, NaN and infinities too:
-// the producer overwrites them with zeros in shared memory before the block
-// is used (0 * NaN in P V would reach the output), and their logits are
-// masked by selection, not by adding.
+// their logits are masked by selection, and the producer overwrites them with
+// zeros in V entries before the MMA reads those (0 * NaN would reach O).
+//
+// Warp roles: 0 and 2 load by TMA; 1 of CTA 0 issues every MMA (one elected lane), 1
+// of CTA 1 passes on its CTA's arrivals to CTA 0; 4-11 run the softmax and the
+// epilogue.
 #pragma once
 
 #include "layout.cuh"
-#include "sparse_attn_vh.cuh"
+#include "ptx.cuh"
+
+#include <cuda_bf16.h>
 
 namespace dsa {
 
 struct DenseParams {
-  const __nv_bfloat16* q;      // [rows, H, 576]
   KeyMap km;
   RowPos rp;
   const int32_t* kv_len;
@@ -47,24 +66,39 @@ struct DenseParams {
   int32_t min_share;           // blocks
   float scale_log2;
 
-  // Keys that query row r sees, and the 64-key blocks they fill.
+  // Keys that query row r sees, and the 128-key blocks they fill.
   __device__ __forceinline__ int visible(int r) const {
     const int b = r / n_q;
     const int last = min(rp.pos(b, r - b * n_q), n_kv - 1);     // no overflow at INT_MAX
     const int len = kv_len ? kv_len[b] : n_kv;
     return max(0, min(last + 1, len));
   }
-  __device__ __forceinline__ int blocks(int r) const { return (visible(r) + 63) >> 6; }
+  __device__ __forceinline__ int blocks(int r) const { return (visible(r) + 127) >> 7; }
   __device__ __forceinline__ long long share(long long total) const {
     return max(static_cast<long long>(min_share), (total + pairs - 1) / pairs);
   }
 };
 
-struct DenseTile : VhTile {
-  static constexpr int THREADS = 384;           // TMA 0, S MMA 1, PV MMA 2, softmax 4-11
-  static constexpr int AHEAD = 5;               // blocks whose lines are on their way into L2
-  static constexpr int SM0 = 4;                 // first softmax warp
-  static constexpr int NUM_BARS = 4 * STAGES + 8;
+struct DenseTile {
+  static constexpr int NK = 128;                // keys per block, 64 loaded by each CTA for S
+  static constexpr int HB = 64;                 // heads per CTA
+  static constexpr int DQK = 576, DV = 512;
+  static constexpr int QB = DQK / 64;           // 9 dim blocks of Q
+  static constexpr int BOX = 64 * 128;          // 64 rows x 64 dims
+  static constexpr int ENTRY = 2 * BOX;
+  static constexpr int RING = 8;
+  static constexpr int SE = 5, VE = 4;          // entries of S, of V per block
+  static constexpr int THREADS = 384;
+  static constexpr int SM0 = 4, SOFTMAX_WARPS = 8;
+  static constexpr int COL_O = 0, COL_S = 256;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr int OFF_RING = 0;
+  static constexpr int OFF_Q = RING * ENTRY;
+  static constexpr int OFF_P = OFF_Q + QB * BOX;               // [2 key halves][64 heads][64 keys]
+  static constexpr int P_BYTES = HB * NK * 2;
+  static constexpr int OFF_RED = OFF_P + P_BYTES;              // [2 parity][4 parts][64 heads] fp32
+  static constexpr int OFF_BAR = OFF_RED + 2 * 4 * HB * 4;
+  static constexpr int NUM_BARS = 3 * RING + 10;
   static constexpr int OFF_SCAN = OFF_BAR + NUM_BARS * 8;      // [12] sums, then the start
   static constexpr int SMEM_BYTES = OFF_SCAN + 12 * 8 + 32;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -96,7 +130,7 @@ struct DenseWalk {
     if (left <= 0) return false;
     int v = p.visible(row);
     while (v == 0) v = p.visible(++row);     // blocks are left, so such a row follows
-    const int nb = (v + 63) >> 6;
+    const int nb = (v + 127) >> 7;
     s.row = row;
     s.blk = blk;
     s.n = static_cast<int>(min(left, static_cast<long long>(nb - blk)));
@@ -109,59 +143,63 @@ struct DenseWalk {
   }
 };
 
-// tmap_kv: the cache as bf16 rows of 576, box 64 dims x 64 rows. tmap_o and
-// tmap_p: out and part_o as byte rows of 512 elements, box 128 bytes x H rows.
-// All with the 128-byte swizzle.
-__global__ void __launch_bounds__(384, 1)
+// tmap_kv: the cache as [9 dim blocks][rows][64], box 64 dims x 64 rows x 2
+// blocks (blocks past the ninth read as zero). tmap_q: Q as
+// [rows][H][576], box 64 dims x 64 heads. tmap_o, tmap_p: out and part_o as
+// [rows or slots][H][512 elements in bytes], box 128 bytes x 64 heads. All with
+// the 128-byte swizzle; heads past H read as zero and are not stored.
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     dense_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv,
+                      const __grid_constant__ CUtensorMap tmap_q,
                       const __grid_constant__ CUtensorMap tmap_o,
                       const __grid_constant__ CUtensorMap tmap_p, const DenseParams p) {
   using T = DenseTile;
   constexpr int NK = T::NK;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
-  uint8_t* c_smem = smem + T::OFF_C;
-  uint8_t* qs_smem = smem + T::OFF_QS;
+  uint8_t* ring = smem + T::OFF_RING;
+  uint8_t* q_smem = smem + T::OFF_Q;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_BAR);
-  uint64_t* cx_full = bars;                      // [2] logit-only blocks of the stage landed
-  uint64_t* cv_full = bars + T::STAGES;          // [2] V-half blocks landed
-  uint64_t* cx_empty = bars + 2 * T::STAGES;     // [2] S of the stage's block finished
-  uint64_t* cv_empty = bars + 3 * T::STAGES;     // [2] PV of the stage's block finished
-  uint64_t* s_full = bars + 4 * T::STAGES;       // S tile written
-  uint64_t* s_free = s_full + 1;                 // S tile loaded by all softmax warps
-  uint64_t* p_full = s_full + 2;                 // [2] P tile of buffer b written
-  uint64_t* pv_done = s_full + 4;                // [2] PV of buffer b finished (buffer free, O updated)
-  uint64_t* q_ready = s_full + 6;                // Q of a segment in TMEM and shared memory
-  uint64_t* tail = s_full + 7;                   // a row's last, partly filled block landed
+  uint64_t* full = bars;                         // [RING] this CTA's part of the entry landed
+  uint64_t* far_full = bars + T::RING;           // [RING] (CTA 0) the other CTA's part landed
+  uint64_t* empty = bars + 2 * T::RING;          // [RING] the MMAs have read the entry
+  uint64_t* q_full = bars + 3 * T::RING;         // this CTA's Q of a segment landed
+  uint64_t* far_q = q_full + 1;                  // (CTA 0) the other CTA's Q landed
+  uint64_t* q_empty = q_full + 2;                // the segment's last S has read Q
+  uint64_t* s_full = q_full + 3;                 // [2] S of buffer b written
+  uint64_t* s_free = q_full + 5;                 // [2] (CTA 0) both CTAs' softmax warps have loaded it
+  uint64_t* p_full = q_full + 7;                 // (CTA 0) both CTAs' P written
+  uint64_t* pv_done = q_full + 8;                // O += P V finished
+  uint64_t* tail = q_full + 9;                   // a partly filled V entry landed
   long long* scan = reinterpret_cast<long long*>(smem + T::OFF_SCAN);
-  int* start = reinterpret_cast<int*>(scan + 12);               // row, block of the share's begin
+  int* start = reinterpret_cast<int*>(scan + 12);              // row, block of the share's begin
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 2);
 
-  if ((smem_u32(smem_raw) & 1023u) != 0) {      // see VhTile::SMEM_BYTES: no slack to realign
-    if (threadIdx.x == 0) raise_error(kErrInternal);
-    return;
-  }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int pair = blockIdx.x >> 1, vh = blockIdx.x & 1;
+  const int pair = blockIdx.x >> 1;
+  const uint32_t rank = cluster_ctarank();       // = blockIdx.x & 1
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < T::STAGES; ++s) {
-      mbar_init(&cx_full[s], 1);
-      mbar_init(&cv_full[s], 1);
-      mbar_init(&cx_empty[s], 1);
-      mbar_init(&cv_empty[s], 1);
+    if ((smem_u32(smem_raw) & 1023u) != 0) raise_error(kErrInternal);   // see SMEM_BYTES: no slack
+    for (int s = 0; s < T::RING; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&far_full[s], 1);
+      mbar_init(&empty[s], 1);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, T::SOFTMAX_WARPS);
+    mbar_init(q_full, 1);
+    mbar_init(far_q, 1);
+    mbar_init(q_empty, 1);
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&p_full[s], T::SOFTMAX_WARPS);
-      mbar_init(&pv_done[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&s_free[s], 2 * T::SOFTMAX_WARPS);
     }
-    mbar_init(q_ready, T::SOFTMAX_WARPS);
+    mbar_init(p_full, 2 * T::SOFTMAX_WARPS);
+    mbar_init(pv_done, 1);
     mbar_init(tail, 1);
     fence_mbar_init();
     prefetch_tmap(&tmap_kv);
+    prefetch_tmap(&tmap_q);
   }
   griddep_launch_dependents();                   // the join may be launched (it waits for this grid)
   // ---- the share: blocks [begin, end) of the line of all rows' blocks
@@ -172,7 +210,8 @@ __global__ void __launch_bounds__(384, 1)
   const long long share = p.share(total);
   const long long begin = pair * share;
   DenseWalk walk{0, 0, max(0ll, min(total, begin + share) - begin)};
-  if (walk.left == 0) return;                    // the same in every thread: no TMEM, no copies yet
+  // the same in every thread of both CTAs: no TMEM, no copies yet
+  if (walk.left == 0 || (smem_u32(smem_raw) & 1023u) != 0) return;
   for (long long base = 0, r0 = 0; r0 < p.rows; r0 += T::THREADS) {
     // exclusive prefix of this thread's row within the tile of rows
     const int r = static_cast<int>(r0) + threadIdx.x;
@@ -199,279 +238,250 @@ __global__ void __launch_bounds__(384, 1)
     if (base > begin) break;                     // the same in every thread
   }
   if (warp == 1) {
-    tmem_alloc(tmem_slot, T::TMEM_COLS);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_slot, T::TMEM_COLS);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
+  cluster_sync();                                // also: both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   walk.row = start[0];
   walk.blk = start[1];
 
-  // Every role walks the same segments and counts their blocks alike: g is
-  // the CTA's running block number, which picks the stage, the P buffer and
-  // the barrier phases.
-  if (warp == 0) {
-    // ------------------------------------------------------------ key blocks by TMA
-    uint32_t g = 0, tails = 0;
-    uint32_t nx = 0, nv = 0;                     // loads issued on cx_full, on cv_full
+  // Every role walks the same segments and counts alike: g is the pair's
+  // running block number, e the running ring entry. In a segment of n blocks
+  // the entries are those of S(0), S(1), V(0), S(2), V(1), ..., V(n - 1).
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------ loads
+    // Warp 0 loads Q and the S entries, warp 2 the V entries: issuing a copy
+    // takes one thread about 290 cycles, nine of them would bound a block.
+    // Both walk every entry and wait until it is free, so that a barrier is
+    // never two phases ahead of a waiting thread.
+    const bool for_s = warp == 0;
+    uint32_t e = 0, segs = 0, tails = 0;
+    uint32_t mine = 0, phase = 0;                // slots this warp has filled, and their phases
     bool ok = true;
     DenseSeg w;
+    // One entry: waits until its slot is free and returns it.
+    auto slot_free = [&]() -> uint32_t {
+      const uint32_t st = e % T::RING;
+      ok = mbar_wait(&empty[st], ((e / T::RING) & 1) ^ 1);
+      return st;
+    };
+    auto filled = [&](uint32_t st) {
+      mine |= 1u << st;
+      phase = (phase & ~(1u << st)) | (((e / T::RING) & 1) << st);
+    };
     while (ok && walk.next(p, w)) {
       const int b = w.row / p.n_q;
-      // The pool row of a block's first key: a block of 64 lies inside one
+      // The pool row of a block's first key: a block of 128 lies inside one
       // page. A page outside the pool reads as zeros (the rows past the end).
       auto locate = [&](int blk) -> int {
         const int64_t r = p.km.row(b, blk * NK, p.n_kv);
         return static_cast<int>(r >= 0 ? r : p.km.pool_rows);
       };
-      int at = locate(w.blk);
-      for (int i = 0; i < w.n; ++i, ++g) {
-        const int blk = w.blk + i;
-        const int st = g % T::STAGES;
-        const uint32_t ph = ((g / T::STAGES) & 1) ^ 1;
-        const int valid = w.vis - blk * NK;
-        const int y = at;
-        if (i + 1 < w.n) at = locate(blk + 1);   // one block ahead
-        uint8_t* dst = c_smem + st * T::STAGE_BYTES;
-        if (i + T::AHEAD < w.n) {
-          const int yp = locate(blk + T::AHEAD);
-          if (lane < T::NDB && (lane & 1) == vh) tma_prefetch_2d(&tmap_kv, lane * 64, yp);
-        }
-        ok = mbar_wait(&cx_empty[st], ph);
+      if (for_s) {
+        // Q of this CTA's heads, once the previous segment's last S has read it
+        if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1);
         if (!ok) break;
-        if (valid >= NK) {
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&cx_full[st], T::XDB * T::DB_BYTES);
-#pragma unroll
-            for (int t = 0; t < T::XDB; ++t) {
-              const int db = t == 4 ? 8 : t + 4 * (1 - vh);
-              tma_load_2d(dst + db * T::DB_BYTES, &tmap_kv, &cx_full[st], db * 64, y);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_full, T::QB * T::BOX);
+          for (int t = 0; t < T::QB; ++t)
+            tma_load_3d(q_smem + t * T::BOX, &tmap_q, q_full, t * 64, static_cast<int>(rank) * T::HB, w.row);
+        }
+      }
+      ++segs;
+      int y = locate(w.blk);                     // of the block this warp loads next
+      for (int i = 0; i <= w.n && ok; ++i) {
+        if (i < w.n) {
+          // S(i): this CTA's 64 keys, dims 128 t .. + 127 (the last entry: 64)
+          for (int t = 0; t < T::SE; ++t, ++e) {
+            const uint32_t st = slot_free();
+            if (!ok) break;
+            if (!for_s) continue;
+            filled(st);
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[st], T::ENTRY);
+              tma_load_3d(ring + st * T::ENTRY, &tmap_kv, &full[st], 0, y + static_cast<int>(rank) * 64, 2 * t);
             }
           }
-          ++nx;
-          ok = mbar_wait(&cv_empty[st], ph);
           if (!ok) break;
-          ++nv;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&cv_full[st], T::VDB * T::DB_BYTES);
-#pragma unroll
-            for (int t = 0; t < T::VDB; ++t) {
-              const int db = 4 * vh + t;
-              tma_load_2d(dst + db * T::DB_BYTES, &tmap_kv, &cv_full[st], db * 64, y);
+          if (for_s && i + 1 < w.n) y = locate(w.blk + i + 1);
+        }
+        if (i == 0) continue;
+        // V(i - 1): entry (key half kh, accumulator j): dims 256 j + 128 rank .. + 127
+        const int valid = w.vis - (w.blk + i - 1) * NK;
+        for (int t = 0; t < T::VE; ++t, ++e) {
+          const uint32_t st = slot_free();
+          if (!ok) break;
+          if (for_s) continue;
+          filled(st);
+          const int kh = t >> 1, zb = 4 * (t & 1) + 2 * static_cast<int>(rank);
+          const int rows = valid - 64 * kh;      // of this half that hold keys
+          uint8_t* dst = ring + st * T::ENTRY;
+          if (rows >= 64 || rows <= 0) {
+            // a half without keys reads as zeros: past the end of the pool
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&full[st], T::ENTRY);
+              tma_load_3d(dst, &tmap_kv, &full[st], 0, rows > 0 ? y + 64 * kh : static_cast<int>(p.km.pool_rows), zb);
             }
-          }
-        } else {
-          ok = mbar_wait(&cv_empty[st], ph);
-          if (!ok) break;
-          if (lane == 0) {
-            mbar_arrive_expect_tx(tail, T::NDB * T::DB_BYTES);
-            for (int db = 0; db < T::NDB; ++db)
-              tma_load_2d(dst + db * T::DB_BYTES, &tmap_kv, tail, db * 64, y);
-          }
-          ok = mbar_wait(tail, tails & 1);
-          if (!ok) {
-            mbar_wait(tail, tails & 1);          // in flight: once more before the CTA ends
-            break;
-          }
-          ++tails;
-          ++nx;
-          ++nv;
-          // rows valid .. 63 of every box become zeros
-          const int words = (NK - valid) * 8;    // 16-byte words per box
-          for (int db = 0; db < T::NDB; ++db) {
-            const uint32_t a = smem_u32(dst) + db * T::DB_BYTES + valid * 128;
-            for (int k = lane; k < words; k += 32) sts_v4(a + k * 16, 0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&cx_full[st]);
-            mbar_arrive(&cv_full[st]);
+          } else {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(tail, T::ENTRY);
+              tma_load_3d(dst, &tmap_kv, tail, 0, y + 64 * kh, zb);
+            }
+            ok = mbar_wait(tail, tails & 1) || mbar_wait(tail, tails & 1);
+            ++tails;
+            for (int k = lane; k < (64 - rows) * 8; k += 32) {
+              sts_v4(smem_u32(dst) + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
+              sts_v4(smem_u32(dst) + T::BOX + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[st]);
           }
         }
-        __syncwarp();
+        if (!for_s && i < w.n) y = locate(w.blk + i);
       }
+      __syncwarp();
     }
-    // A wait that ran out leaves copies in flight: they end before the CTA does
-    // (the last two uses of each barrier).
-    if (!ok)
-      for (uint32_t d = 1; d <= 2; ++d) {
-        if (nx >= d) mbar_wait(&cx_full[(nx - d) % T::STAGES], ((nx - d) / T::STAGES) & 1);
-        if (nv >= d) mbar_wait(&cv_full[(nv - d) % T::STAGES], ((nv - d) / T::STAGES) & 1);
-      }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ S = Q K^T issuer
-    // One elected lane runs the whole loop (see elect_one). Descriptors are
-    // formed once: adding (byte offset >> 4) moves the start address.
+    // A wait that ran out leaves copies in flight: they end before the CTA does.
+    if (!ok) {
+      for (uint32_t st = 0; st < T::RING; ++st)
+        if ((mine >> st) & 1u) mbar_wait(&full[st], (phase >> st) & 1u);
+      if (for_s && segs > 0) mbar_wait(q_full, (segs - 1) & 1);
+    }
+  } else if (warp == 1 && rank == 1) {
+    // ------------------------------------------------------------ arrivals passed on to CTA 0
     if (elect_one()) {
-      constexpr uint32_t idesc_s = umma_idesc(128, NK, 1u, 1u, 0u, 0u);
-      const uint64_t c_desc0 = umma_desc(smem_u32(c_smem), 16, 1024, 2);
-      const uint64_t q_desc0 = umma_desc(smem_u32(qs_smem), 16, 1024, 2);
-      const uint32_t d_s = tmem_base + T::COL_S;
-      const uint32_t x_shift = static_cast<uint32_t>(4 * (1 - vh) * T::DB_BYTES) >> 4;
-      const uint32_t v_shift = static_cast<uint32_t>(4 * vh * T::DB_BYTES) >> 4;
-      uint32_t g = 0, k = 0;
+      uint32_t e = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
       while (ok && walk.next(p, w)) {
-        ok = mbar_wait(q_ready, k & 1);
-        ++k;
-        tc_fence_after();
-        for (int i = 0; i < w.n && ok; ++i, ++g) {
-          const int st = g % T::STAGES;
-          const uint32_t ph = (g / T::STAGES) & 1;
-          // the S buffer is free once every softmax warp has loaded S(g - 1)
-          ok = (g == 0 || mbar_wait(s_free, (g - 1) & 1)) && mbar_wait(&cx_full[st], ph);
+        ok = mbar_wait(q_full, segs & 1);
+        if (!ok) break;
+        mbar_arrive_at(far_q, 0);
+        ++segs;
+        const uint32_t last = e + static_cast<uint32_t>(w.n) * (T::SE + T::VE);
+        for (; e < last; ++e) {
+          ok = mbar_wait(&full[e % T::RING], (e / T::RING) & 1);
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t cd = c_desc0 + static_cast<uint32_t>(st * (T::STAGE_BYTES >> 4));
-#pragma unroll
-          for (int t = 0; t < T::XDB; ++t)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint32_t off = (t < 4 ? t * T::DB_BYTES : 8 * T::DB_BYTES) + kk * 32;
-              const uint64_t bd = cd + (t < 4 ? x_shift : 0u) + (off >> 4);
-              umma_bf16_ts(d_s, tmem_base + T::COL_Q + t * 32 + kk * 8, bd, idesc_s,
-                           (t | kk) ? 1u : 0u);
-            }
-          umma_commit(&cx_empty[st]);
-          ok = mbar_wait(&cv_full[st], ph);
-          if (!ok) break;
-          tc_fence_after();
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t bd = cd + v_shift + ((kk * 32) >> 4);
-            umma_bf16_ts(d_s, tmem_base + T::COL_Q + T::XDB * 32 + kk * 8, bd, idesc_s, 1u);
-          }
-#pragma unroll
-          for (int uq = 0; uq < T::QSB; ++uq)
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ad = q_desc0 + ((uq * T::M * 128 + kk * 32) >> 4);
-              const uint64_t bd = cd + v_shift + (((uq + 1) * T::DB_BYTES + kk * 32) >> 4);
-              umma_bf16_ss(d_s, ad, bd, idesc_s, 1u);
-            }
-          umma_commit(s_full);
+          mbar_arrive_at(&far_full[e % T::RING], 0);
         }
       }
     }
     __syncwarp();
-  } else if (warp == 2) {
-    // ------------------------------------------------------------ O += P V issuer
-    // P(g) exists only after S(g) was read, so when PV(g) completes both
-    // readers of the V-half blocks are done and P buffer g & 1 is free. The
-    // first PV of a segment overwrites O: the softmax warps write its P only
-    // after they have read out the previous segment's O.
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer (CTA 0)
     if (elect_one()) {
-      constexpr uint32_t idesc_pv = umma_idesc(128, T::VH, 1u, 1u, 0u, 1u);
+      constexpr uint32_t idesc_s = umma_idesc(128, NK, 1u, 1u, 0u, 0u);
+      constexpr uint32_t idesc_pv = umma_idesc(128, 256, 1u, 1u, 0u, 1u);
+      const uint64_t k_desc0 = umma_desc(smem_u32(ring), 16, 1024, 2);
+      const uint64_t v_desc0 = umma_desc(smem_u32(ring), T::BOX, 1024, 2);
+      const uint64_t q_desc0 = umma_desc(smem_u32(q_smem), 16, 1024, 2);
       const uint64_t p_desc0 = umma_desc(smem_u32(smem + T::OFF_P), 16, 1024, 2);
-      const uint64_t v_desc0 = umma_desc(smem_u32(c_smem) + 4 * vh * T::DB_BYTES, T::DB_BYTES, 1024, 2);
-      uint32_t g = 0;
+      uint32_t e = 0, g = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
+      auto landed = [&]() {
+        const uint32_t st = e % T::RING, ph = (e / T::RING) & 1;
+        ok = mbar_wait(&full[st], ph) && mbar_wait(&far_full[st], ph);
+        tc_fence_after();
+        return ok;
+      };
       while (ok && walk.next(p, w)) {
-        for (int i = 0; i < w.n; ++i, ++g) {
-          const int st = g % T::STAGES;
-          if (!(ok = mbar_wait(&p_full[g & 1], (g >> 1) & 1))) break;
-          tc_fence_after();
-          const uint64_t vd = v_desc0 + static_cast<uint32_t>(st * (T::STAGE_BYTES >> 4));
-          const uint64_t pd = p_desc0 + static_cast<uint32_t>((g & 1) * (T::P_BYTES >> 4));
+        ok = mbar_wait(q_full, segs & 1) && mbar_wait(far_q, segs & 1);
+        ++segs;
+        tc_fence_after();
+        for (int i = 0; i <= w.n && ok; ++i) {
+          if (i < w.n) {
+            // S(g + i) into buffer b, free once S(g + i - 2) has been loaded
+            const uint32_t gs = g + i, b = gs & 1;
+            if (gs > 1) ok = mbar_wait(&s_free[b], ((gs >> 1) & 1) ^ 1);
+            tc_fence_after();
+            const uint32_t d = tmem_base + T::COL_S + b * 64;
 #pragma unroll
-          for (int kk = 0; kk < NK / 16; ++kk)
-            umma_bf16_ss(tmem_base + T::COL_O, pd + ((kk * 32) >> 4), vd + ((kk * 2048) >> 4),
-                         idesc_pv, (i > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&cv_empty[st]);
-          umma_commit(&pv_done[g & 1]);
+            for (int t = 0; t < T::SE; ++t) {
+              if (!landed()) break;
+              const uint64_t kd = k_desc0 + static_cast<uint32_t>((e % T::RING) * (T::ENTRY >> 4));
+#pragma unroll
+              for (int kk = 0; kk < (t < 4 ? 8 : 4); ++kk) {
+                const uint32_t off = ((kk >> 2) * T::BOX + (kk & 3) * 32) >> 4;
+                umma_bf16_ss_pair(d, q_desc0 + (t * (T::ENTRY >> 4) + off), kd + off, idesc_s,
+                                  (t | kk) ? 1u : 0u);
+              }
+              umma_commit_pair(&empty[e % T::RING]);
+              ++e;
+            }
+            if (!ok) break;
+            umma_commit_pair(&s_full[b]);
+            if (i + 1 == w.n) umma_commit_pair(q_empty);
+          }
+          if (i == 0) continue;
+          // O += P V of block g + i - 1
+          const uint32_t gp = g + i - 1;
+          if (!(ok = mbar_wait(p_full, gp & 1))) break;
+          tc_fence_after();
+          const uint32_t more_o = i > 1 ? 1u : 0u;   // a segment's first product overwrites O
+#pragma unroll
+          for (int t = 0; t < T::VE; ++t) {
+            if (!landed()) break;
+            const uint64_t vd = v_desc0 + static_cast<uint32_t>((e % T::RING) * (T::ENTRY >> 4));
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              umma_bf16_ss_pair(tmem_base + T::COL_O + (t & 1) * 128,
+                                p_desc0 + (((t >> 1) * T::BOX + kk * 32) >> 4), vd + ((kk * 2048) >> 4),
+                                idesc_pv, (t > 1 || kk > 0) ? 1u : more_o);
+            umma_commit_pair(&empty[e % T::RING]);
+            ++e;
+          }
+          if (ok) umma_commit_pair(pv_done);
         }
+        g += w.n;
       }
     }
     __syncwarp();
   } else if (warp >= T::SM0) {
     // ------------------------------------------------------------ softmax / epilogue
     const int quarter = warp & 3;
-    const int half = (warp - T::SM0) >> 2;                   // which 32 keys of a block
-    const int h = quarter * 32 + lane;                       // head row = TMEM lane
+    const int half = (warp - T::SM0) >> 2;                   // which 32 of a lane's 64 keys
+    const int row = quarter * 32 + lane;                     // TMEM lane
+    const int h = row & 63, side = row >> 6;                 // head of this CTA; key / dim half
+    const int part = side * 2 + half;                        // of the four threads of a head
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
-    const uint32_t pair_bar = 1u + static_cast<uint32_t>(quarter);   // the quarter's two warps
-    float* red = reinterpret_cast<float*>(smem + T::OFF_RED);   // [parity][half][128]
+    const uint32_t head_bar = 1u + static_cast<uint32_t>(quarter & 1);   // the four warps of its heads
+    float* red = reinterpret_cast<float*>(smem + T::OFF_RED);   // [parity][part][64]
     const int stid = threadIdx.x - T::SM0 * 32;              // 0..255 over the softmax warps
     constexpr uint32_t kAllBar = 5u;                         // named barrier of the 8 warps
     constexpr uint32_t kAllThreads = 32u * T::SOFTMAX_WARPS;
-
-    // Q of a row, three 64-dim blocks at a time through the Q area of shared
-    // memory: twice as staging for the six TMEM blocks, once for the three
-    // that stay there.
-    auto copy_q3 = [&](int row, int first, bool tmem_part) {
-      const __nv_bfloat16* qrow = p.q + static_cast<size_t>(row) * p.H * T::DQK;
-      const int r4 = stid >> 3, ch = stid & 7;
-#pragma unroll
-      for (int j = 0; j < 3; ++j) {
-        const int db = tmem_part ? vh_tblock(first + j, vh) : vh_sblock(first + j, vh);
-#pragma unroll
-        for (int it = 0; it < T::M / 32; ++it) {
-          const int r = it * 32 + r4;
-          const __nv_bfloat16* src = qrow + static_cast<size_t>(min(r, p.H - 1)) * T::DQK + db * 64 + ch * 8;
-          const uint32_t dst = smem_u32(qs_smem) + j * (T::M * 128) + (r >> 3) * 1024 + (r & 7) * 128 +
-                               ((ch ^ (r & 7)) << 4);
-          cp_async_16(dst, src, r < p.H ? 16u : 0u);
-        }
-      }
-      cp_async_wait_all();
-    };
-    auto load_q = [&](int row) {
-#pragma unroll 1
-      for (int round = 0; round < 2; ++round) {
-        copy_q3(row, 3 * round, true);
-        named_bar_sync(kAllBar, kAllThreads);
-#pragma unroll
-        for (int j = 0; j < 3; ++j) {
-          const uint32_t rowp = smem_u32(qs_smem) + j * (T::M * 128) + (h >> 3) * 1024 + (h & 7) * 128;
-          uint32_t v[16];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const uint4 x = lds_v4(rowp + (((4 * half + c) ^ (h & 7)) << 4));
-            v[4 * c] = x.x; v[4 * c + 1] = x.y; v[4 * c + 2] = x.z; v[4 * c + 3] = x.w;
-          }
-          tmem_st16(tmem_base + lane_addr + T::COL_Q + (2 * (3 * round + j) + half) * 16, v);
-        }
-        named_bar_sync(kAllBar, kAllThreads);      // staging read before it is overwritten
-      }
-      copy_q3(row, 0, false);
-      fence_proxy_async_smem();
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
-    };
+    const int head = static_cast<int>(rank) * T::HB + h;     // of the row
 
     uint32_t sr[32];
     float z[32];
-    const uint32_t p_row = smem_u32(smem + T::OFF_P) + (h >> 3) * 1024 + (h & 7) * 128;
+    const uint32_t p_row = smem_u32(smem + T::OFF_P) + side * T::BOX + (h >> 3) * 1024 + (h & 7) * 128;
     uint32_t g = 0;
     bool ok = true;
     DenseSeg w;
     bool more = walk.next(p, w);
-    if (more) load_q(w.row);
     while (more && ok) {
       float m_used = -INFINITY;   // running max (log2 domain) the P values are relative to
-      float l = 0.f;              // this warp's share of the sum of the fp32 p (LSE)
+      float l = 0.f;              // this thread's share of the sum of the fp32 p (LSE)
       float l_mma = 0.f;          // ... of the bf16-rounded p the PV MMA used (normalises O)
       for (int i = 0; i < w.n; ++i, ++g) {
-        // ---- logits of this warp's 32 keys; the S buffer is released at
-        // once. A failed wait does not leave the loop before the partner
-        // exchange: the quarter's two warps leave together.
-        const int valid = w.vis - (w.blk + i) * NK - half * 32;   // of this warp's 32 keys
-        if (ok) ok = mbar_wait(s_full, g & 1);
+        // ---- logits of this thread's 32 keys; the S buffer is released at
+        // once. A failed wait does not leave the loop before the exchange:
+        // the four warps of a head leave together.
+        const uint32_t b = g & 1;
+        const int valid = w.vis - (w.blk + i) * NK - part * 32;
+        if (ok) ok = mbar_wait(&s_full[b], (g >> 1) & 1);
         tc_fence_after();
-        tmem_ld32(tmem_base + lane_addr + T::COL_S + half * 32, sr);
+        tmem_ld32(tmem_base + lane_addr + T::COL_S + b * 64 + half * 32, sr);
         tmem_wait_ld();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
-        // ---- block max over the 64 keys, shared with the partner warp (over
-        // the unscaled logits: the scale is not negative, see the host's check)
+        if (lane == 0) mbar_arrive_at(&s_free[b], 0);
+        // ---- block max over the 128 keys, shared among the head's threads
+        // (over the unscaled logits: the scale is positive)
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(sr[j]);
         if (valid < 32) {
@@ -485,23 +495,23 @@ __global__ void __launch_bounds__(384, 1)
           mx[r] = fmaxf(fmaxf(fmaxf(z[r], z[r + 4]), fmaxf(z[r + 8], z[r + 12])),
                         fmaxf(fmaxf(z[r + 16], z[r + 20]), fmaxf(z[r + 24], z[r + 28])));
         const float hmax = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-        float* red_i = red + (g & 1) * (2 * T::M);
-        red_i[half * T::M + h] = hmax;
-        if (!named_bar_and(pair_bar, 64u, ok)) {
+        float* red_i = red + (g & 1) * (4 * T::HB) + h;
+        red_i[part * T::HB] = hmax;
+        if (!named_bar_and(head_bar, 128u, ok)) {
           ok = false;
           break;
         }
-        const float bmax = fmaxf(hmax, red_i[(half ^ 1) * T::M + h]);
-        // ---- online softmax. Rescaling O needs PV(g - 1) finished; writing
-        // P buffer g & 1 needs PV(g - 2) finished.
+        const float bmax = fmaxf(fmaxf(red_i[0], red_i[T::HB]), fmaxf(red_i[2 * T::HB], red_i[3 * T::HB]));
+        // ---- online softmax: both rescaling O and writing P need PV(g - 1)
+        // finished
         const bool grow = bmax > m_used + 8.0f;
         const float m_new = grow ? bmax : m_used;
+        if (g > 0 && ok) ok = mbar_wait(pv_done, (g - 1) & 1);
         if (i > 0 && __any_sync(0xffffffffu, grow)) {
-          if (ok) ok = mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
           tc_fence_after();
           const float alpha = grow ? ex2_approx(m_used - m_new) : 1.0f;
 #pragma unroll 1
-          for (int c = half * (T::VH / 2); c < (half + 1) * (T::VH / 2) && ok; c += 16) {
+          for (int c = half * 128; c < (half + 1) * 128 && ok; c += 16) {
             uint32_t o[16];
             tmem_ld16(tmem_base + lane_addr + T::COL_O + c, o);
             tmem_wait_ld();
@@ -512,8 +522,6 @@ __global__ void __launch_bounds__(384, 1)
           tmem_wait_st();
           l *= alpha;
           l_mma *= alpha;
-        } else if (g > 1 && ok) {
-          ok = mbar_wait(&pv_done[g & 1], ((g >> 1) & 1) ^ 1);
         }
         m_used = m_new;
         uint32_t pk[16];
@@ -536,69 +544,65 @@ __global__ void __launch_bounds__(384, 1)
         }
         l += lsum;
         l_mma += lsum_mma;
-        const uint32_t pb = p_row + (g & 1) * T::P_BYTES;
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          sts_v4(pb + (((4 * half + c) ^ (h & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2],
+          sts_v4(p_row + (((4 * half + c) ^ (h & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2],
                  pk[4 * c + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[g & 1]);
+        if (lane == 0) mbar_arrive_at(p_full, 0);
       }
       // all softmax warps go on, or stop, together
       if (!named_bar_and(kAllBar, kAllThreads, ok)) {
         ok = false;
         break;
       }
-      // ---- the next segment's Q: this segment's S MMAs have all completed
-      // (the last S was loaded above), so its logits may start during this
-      // epilogue
       const DenseSeg done = w;
       more = walk.next(p, w);
-      if (more) load_q(w.row);
       // ---- epilogue: O of the segment, once its last PV has finished
-      ok = mbar_wait(&pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1);
+      ok = mbar_wait(pv_done, (g - 1) & 1);
       tc_fence_after();
-      red[half * T::M + h] = l;
-      red[(2 + half) * T::M + h] = l_mma;
-      named_bar_sync(pair_bar, 64u);
-      const float l_o = red[(half ^ 1) * T::M + h];
-      const float lm_o = red[(2 + (half ^ 1)) * T::M + h];
-      const bool pv_ok = ok;
-      named_bar_sync(pair_bar, 64u);
-      const float l_all = half == 0 ? l + l_o : l_o + l;
-      const float lm_all = half == 0 ? l_mma + lm_o : lm_o + l_mma;
+      red[part * T::HB + h] = l;
+      red[(4 + part) * T::HB + h] = l_mma;
+      const bool pv_ok = named_bar_and(kAllBar, kAllThreads, ok);
+      float l_all = 0.f, lm_all = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        l_all += red[k * T::HB + h];
+        lm_all += red[(4 + k) * T::HB + h];
+      }
+      named_bar_sync(kAllBar, kAllThreads);      // read before the next segment's maxima
       // O / sum(rounded p) is an exact convex combination of the V rows; the
       // LSE keeps the unrounded sum.
       const bool has = pv_ok && l_all != 0.f && lm_all != 0.f;   // true for NaN
       const float inv_l = has ? 1.0f / lm_all : 0.f;
       const uint32_t keep = has ? 0xffffffffu : 0u;
       const float lse_v = has ? (m_used + log2f(l_all)) * 0.69314718055994531f : -INFINITY;
-      // O leaves by TMA stores of 128-byte-wide column slices staged in the
-      // swizzled layout the store reads: one slice per round, alternating
-      // between the two P buffers (free: the last PV has finished); after the
-      // last segment all slices at once through the stage area.
+      // O leaves by TMA stores of 128-byte-wide column slices of the 64 heads,
+      // staged in the swizzled layout the store reads. A round covers the
+      // same slice of both lane halves (dims 128 apart): through the P area (free: the
+      // last PV has finished), one round at a time; after the last segment
+      // every round at once through the ring.
       const bool direct = done.whole;
       const int slot = 2 * pair + (done.blk > 0 ? 0 : 1);
       const bool bf16_out = direct && p.out_bf16;
       const int esz = bf16_out ? 2 : 4;
-      const int slice_cols = 128 / esz;
-      const int n_slices = T::VH / slice_cols;
-      const int per_round = more ? 1 : n_slices;
-      const int32_t y_row = (direct ? done.row : slot) * p.H;
+      const int cols = 128 / esz;                // of a slice
+      const int rounds = 256 / cols;             // slices of a lane's 256 columns
+      const int per_step = more ? 1 : rounds;
+      const int z0 = direct ? done.row : slot;
 #pragma unroll 1
-      for (int s0 = 0, rnd = 0; s0 < n_slices; s0 += per_round, ++rnd) {
-        const uint32_t stage =
-            more ? smem_u32(smem + T::OFF_P) + (rnd & 1) * T::P_BYTES : smem_u32(c_smem);
-        if (more && stid == 0) bulk_wait_read<1>();     // the store of round rnd - 2 has read it
-        named_bar_sync(kAllBar, kAllThreads);
-        for (int sl = s0; sl < s0 + per_round; ++sl) {
-          const uint32_t srow = stage + (sl - s0) * (T::M * 128) + h * 128;
+      for (int r0 = 0; r0 < rounds; r0 += per_step) {
+        const uint32_t stage = more ? smem_u32(smem + T::OFF_P) : smem_u32(ring);
+        if (r0 > 0 && stid == 0) bulk_wait_read<0>();    // the last step's stores have read it
+        if (r0 > 0) named_bar_sync(kAllBar, kAllThreads);
+        for (int r = r0; r < r0 + per_step; ++r) {
+          const uint32_t srow = stage + ((r - r0) * 2 + side) * T::BOX + h * 128;
 #pragma unroll 1
-          for (int c = half * (slice_cols / 2); c < (half + 1) * (slice_cols / 2); c += 16) {
+          for (int c = half * (cols / 2); c < (half + 1) * (cols / 2); c += 16) {
             uint32_t o[16];
-            tmem_ld16(tmem_base + lane_addr + T::COL_O + sl * slice_cols + c, o);
+            tmem_ld16(tmem_base + lane_addr + T::COL_O + r * cols + c, o);
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j] & keep) * inv_l);
@@ -625,19 +629,25 @@ __global__ void __launch_bounds__(384, 1)
         }
         fence_proxy_async_smem();
         named_bar_sync(kAllBar, kAllThreads);
-        if (stid == 0) {
+        if (stid == 0 && static_cast<int>(rank) * T::HB < p.H) {
           const void* map = direct ? static_cast<const void*>(&tmap_o) : static_cast<const void*>(&tmap_p);
-          for (int sl = s0; sl < s0 + per_round; ++sl)
-            tma_store_2d(map, stage + (sl - s0) * (T::M * 128), (vh * T::VH + sl * slice_cols) * esz, y_row);
+          for (int r = r0; r < r0 + per_step; ++r)
+#pragma unroll
+            for (int sd = 0; sd < 2; ++sd) {
+              // lane half sd of columns [r cols, + cols): accumulator j = column / 128
+              const int col = r * cols;
+              const int dim = (col >> 7) * 256 + sd * 128 + (col & 127);
+              tma_store_3d(map, stage + ((r - r0) * 2 + sd) * T::BOX, dim * esz,
+                           static_cast<int>(rank) * T::HB, z0);
+            }
           bulk_commit();
         }
       }
       // every staged byte read before the next segment writes P
       if (stid == 0) bulk_wait_read<0>();
-      named_bar_sync(kAllBar, kAllThreads);
-      if (vh == 0 && half == 0 && h < p.H) {
-        if (!direct) p.part_lse[static_cast<size_t>(slot) * p.H + h] = lse_v;
-        else if (p.lse) p.lse[static_cast<size_t>(done.row) * p.H + h] = lse_v;
+      if (part == 0 && head < p.H) {
+        if (!direct) p.part_lse[static_cast<size_t>(slot) * p.H + head] = lse_v;
+        else if (p.lse) p.lse[static_cast<size_t>(done.row) * p.H + head] = lse_v;
       }
       ok = named_bar_and(kAllBar, kAllThreads, ok);
     }
@@ -645,10 +655,11 @@ __global__ void __launch_bounds__(384, 1)
 
   if (threadIdx.x == T::SM0 * 32) bulk_wait<0>();   // the output stores have completed
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  cluster_sync();                                // no arrival or MMA of the pair is outstanding
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, T::TMEM_COLS);
+    tmem_dealloc_pair(tmem_base, T::TMEM_COLS);
   }
 }
 

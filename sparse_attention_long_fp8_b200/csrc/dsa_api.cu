@@ -748,19 +748,26 @@ DensePlan plan_dense(const dsa_shape* s) {
   return d;
 }
 
-// The latent cache as bf16 rows of 576, box 64 dims x 64 rows, 128-byte swizzle.
-dsa_status make_tmap_latent(CUtensorMap* map, const void* base, uint64_t rows) {
+// A 3D tensor for the dense attention's TMA copies: 128-byte swizzle, a box of
+// 128 bytes x 64 rows x depth. dims and strides (bytes, of dims 1..) as
+// cuTensorMapEncodeTiled takes them.
+dsa_status make_tmap_dense(CUtensorMap* map, CUtensorMapDataType type, const void* base,
+                           const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t depth) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint64_t dims[2] = {576, rows};
-  const cuuint64_t strides[1] = {1152};
-  const cuuint32_t box[2] = {64, 64};
-  const cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides,
-                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t box[3] = {type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 128u : 64u, 64, depth};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return DSA_OK;
+}
+// [rows][heads][width bytes]
+dsa_status make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint32_t heads, uint32_t width) {
+  const cuuint64_t dims[3] = {width, heads, rows};
+  const cuuint64_t strides[2] = {width, static_cast<cuuint64_t>(width) * heads};
+  return make_tmap_dense(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, 1);
 }
 
 dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_t* q,
@@ -771,7 +778,6 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   if (dsa_status st = set_smem(dsa::dense_attn_kernel, T::SMEM_BYTES, dev, attr_done)) return st;
   const DensePlan pl = plan_dense(s);
   dsa::DenseParams p{};
-  p.q = reinterpret_cast<const __nv_bfloat16*>(q);
   p.km = lay.km;
   p.rp = dsa::RowPos{q_pos0, lay.row_pos, s->n_q};
   p.kv_len = kv_len;
@@ -785,19 +791,19 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   p.H = s->heads;
   p.out_bf16 = out_bf16;
   p.pairs = pl.pairs;
-  p.min_share = 2;
+  p.min_share = 1;
   p.scale_log2 = s->softmax_scale * 1.4426950408889634f;
-  CUtensorMap tkv, to, tp;
-  if (dsa_status st = make_tmap_latent(&tkv, kv, static_cast<uint64_t>(lay.km.pool_rows))) return st;
-  if (dsa_status st = make_tmap_rows128(&to, out, static_cast<uint64_t>(p.rows) * p.H,
-                                        static_cast<uint32_t>(s->v_dim) * (out_bf16 ? 2u : 4u),
-                                        static_cast<uint32_t>(p.H)))
+  CUtensorMap tkv, tq, to, tp;
+  const cuuint64_t kv_dims[3] = {64, static_cast<cuuint64_t>(lay.km.pool_rows), 9}, kv_strides[2] = {1152, 128};
+  const cuuint64_t q_dims[3] = {576, static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t q_strides[2] = {1152, 1152ull * p.H};
+  if (dsa_status st = make_tmap_dense(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv, kv_dims, kv_strides, 2))
     return st;
-  if (dsa_status st = make_tmap_rows128(&tp, p.part_o, 2ull * pl.pairs * p.H,
-                                        static_cast<uint32_t>(s->v_dim) * 4u,
-                                        static_cast<uint32_t>(p.H)))
+  if (dsa_status st = make_tmap_dense(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, q_dims, q_strides, 1))
     return st;
-  dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, to, tp, p);
+  if (dsa_status st = make_tmap_heads(&to, out, p.rows, p.H, 512 * (out_bf16 ? 2 : 4))) return st;
+  if (dsa_status st = make_tmap_heads(&tp, p.part_o, 2ull * pl.pairs, p.H, 512 * 4)) return st;
+  dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, tq, to, tp, p);
   DSA_CUDA_TRY(cudaGetLastError(), "dense attention launch");
   // the fewer rows, the more partials a row may have
   const int g = p.rows <= 8 ? 8 : (p.rows <= 32 ? 4 : 2);
