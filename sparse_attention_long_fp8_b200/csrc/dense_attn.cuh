@@ -5,13 +5,16 @@
 // when m grows.
 //
 // The work is cut along the caches. All query rows' 128-key blocks, row after
-// row, form one line; CTA pair p takes blocks [p share, (p + 1) share) of it,
+// row, form one line; CTA pair p takes units [p share, (p + 1) share) of it,
 // whatever rows they belong to, so ragged lengths keep every SM equally busy
-// and one long sequence spreads over the whole GPU. A row that lies inside one
+// and one long sequence spreads over the whole GPU. A row counts kDenseRowCost
+// units more than its blocks, at its beginning: taking up a row (its Q, the
+// first block's latency, its output) costs about as much as that many blocks
+// (32 rows of up to 1500 keys: 32.7 us without, 29.2 us with 3). A row that lies inside one
 // share is written directly; the (at most two) rows that a share's ends cut
 // leave an fp32 partial O and LSE in the workspace, and dense_combine_kernel
-// joins them in key order. Both kernels derive the cut from kv_len and the
-// positions on the device: the host never needs the lengths.
+// joins them in key order. The cut is derived from kv_len and the positions on
+// the device: the host never needs the lengths.
 //
 // The two CTAs of a pair (a cluster, two SMs) work on one block together with
 // tcgen05 over both (cta_group::2, M = 128 heads, 64 per CTA):
@@ -30,19 +33,18 @@
 // first half of the N columns of rows 0-63, lanes 64-127 the second half): O
 // 256 columns (two N = 256 accumulators), S 2 x 64.
 //
-// Key blocks stream through one ring of 16 KB entries, one TMA copy each, in the
-// order the MMAs read them: S(i + 1) as five entries (64 keys x 128 dims, the
-// last one 64), then V(i) as four (64 keys x 128 dims). V is loaded a second time
-// (from L2) rather than kept from S: held back until its P exists it would
-// leave no room to load ahead.
+// Key blocks stream through two rings of 16 KB entries, one TMA copy each: S(i)
+// as five entries (64 keys x 128 dims, the last one 64), V(i) as four (64 keys x
+// 128 dims). V is loaded a second time (from L2) rather than kept from S: held
+// back until its P exists it would leave no room to load ahead.
 //
 // Rows behind a sequence's last key may hold anything, NaN and infinities too:
 // their logits are masked by selection, and the producer overwrites them with
 // zeros in V entries before the MMA reads those (0 * NaN would reach O).
 //
 // Warp roles: 0 and 2 load by TMA; 1 of CTA 0 issues every MMA (one elected lane), 1
-// of CTA 1 passes on its CTA's arrivals to CTA 0; 4-11 run the softmax and the
-// epilogue.
+// of CTA 1 passes on its CTA's arrivals to CTA 0; 3 notes the cut and writes the
+// rows that see no key; 4-11 run the softmax and the epilogue.
 #pragma once
 
 #include "layout.cuh"
@@ -52,6 +54,8 @@
 
 namespace dsa {
 
+constexpr int kDenseRowCost = 3;               // blocks
+
 struct DenseParams {
   KeyMap km;
   RowPos rp;
@@ -60,10 +64,10 @@ struct DenseParams {
   float* lse;                  // [rows, H] or null
   float* part_o;               // [2 pairs][H][512]: slot 2 p: the row that share p begins
   float* part_lse;             // [2 pairs][H]       inside of, 2 p + 1: the row it ends inside of
+  int2* cut;                   // [pairs] row and block that share p begins with; row -1: no blocks
   int32_t rows, n_q, n_kv, H;
   int32_t out_bf16;
   int32_t pairs;               // CTA pairs of the attention kernel
-  int32_t min_share;           // blocks
   float scale_log2;
 
   // Keys that query row r sees, and the 128-key blocks they fill.
@@ -74,8 +78,13 @@ struct DenseParams {
     return max(0, min(last + 1, len));
   }
   __device__ __forceinline__ int blocks(int r) const { return (visible(r) + 127) >> 7; }
+  // Its length on the line.
+  __device__ __forceinline__ int units(int r) const {
+    const int nb = blocks(r);
+    return nb > 0 ? nb + kDenseRowCost : 0;
+  }
   __device__ __forceinline__ long long share(long long total) const {
-    return max(static_cast<long long>(min_share), (total + pairs - 1) / pairs);
+    return max(static_cast<long long>(kDenseRowCost + 1), (total + pairs - 1) / pairs);
   }
 };
 
@@ -86,7 +95,8 @@ struct DenseTile {
   static constexpr int QB = DQK / 64;           // 9 dim blocks of Q
   static constexpr int BOX = 64 * 128;          // 64 rows x 64 dims
   static constexpr int ENTRY = 2 * BOX;
-  static constexpr int RING = 8;
+  static constexpr int RS = 4, RV = 4;          // ring entries for S, for V
+  static constexpr int RING = RS + RV;
   static constexpr int SE = 5, VE = 4;          // entries of S, of V per block
   static constexpr int THREADS = 384;
   static constexpr int SM0 = 4, SOFTMAX_WARPS = 8;
@@ -99,60 +109,147 @@ struct DenseTile {
   static constexpr int OFF_RED = OFF_P + P_BYTES;              // [2 parity][4 parts][64 heads] fp32
   static constexpr int OFF_BAR = OFF_RED + 2 * 4 * HB * 4;
   static constexpr int NUM_BARS = 3 * RING + 10;
-  static constexpr int OFF_SCAN = OFF_BAR + NUM_BARS * 8;      // [12] sums, then the start
-  static constexpr int SMEM_BYTES = OFF_SCAN + 12 * 8 + 32;
+  static constexpr int OFF_SCAN = OFF_BAR + NUM_BARS * 8;      // dense_share_block's scratch, TMEM address
+  static constexpr int SMEM_BYTES = OFF_SCAN + (THREADS / 32 + 2) * 8 + 8;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
 };
-
-// Sum of v over the CTA's threads; every thread calls it.
-template <int WARPS>
-__device__ __forceinline__ long long dense_block_sum(long long v, long long* scan) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();               // the previous sum has been read
-  if ((threadIdx.x & 31) == 0) scan[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int i = 0; i < WARPS; ++i) v += scan[i];
-  return v;
-}
 
 // A share's segments: blocks [blk, blk + n) of row `row`, one row after the other.
 struct DenseSeg {
   int row, blk, n, vis;
   bool whole;                    // the row's blocks are all in this segment
 };
+// What is left of a share: `left` units from unit `off` of row `row`.
 struct DenseWalk {
-  int row, blk;
-  long long left;
+  int row;
+  long long off, left;
   __device__ __forceinline__ bool next(const DenseParams& p, DenseSeg& s) {
     if (left <= 0) return false;
     int v = p.visible(row);
-    while (v == 0) v = p.visible(++row);     // blocks are left, so such a row follows
+    while (v == 0) v = p.visible(++row);     // units are left, so such a row follows
     const int nb = (v + 127) >> 7;
+    const long long end = min(off + left, static_cast<long long>(nb + kDenseRowCost));
     s.row = row;
-    s.blk = blk;
-    s.n = static_cast<int>(min(left, static_cast<long long>(nb - blk)));
+    s.blk = static_cast<int>(max(0ll, off - kDenseRowCost));
+    s.n = static_cast<int>(max(0ll, end - kDenseRowCost)) - s.blk;
     s.vis = v;
     s.whole = s.n == nb;
-    left -= s.n;
+    left -= end - off;
     ++row;
-    blk = 0;
-    return true;
+    off = 0;
+    return s.n > 0;                          // 0: the share ends before the row's first block
   }
 };
 
+// The share of pair `pair`. With few rows every warp finds it by itself (32 rows
+// at a time): no barrier, one trip to memory.
+constexpr int kDenseWarpTiles = 8;
+__device__ __forceinline__ DenseWalk dense_share_warp(const DenseParams& p, int pair) {
+  const int lane = threadIdx.x & 31;
+  int len[kDenseWarpTiles];
+#pragma unroll
+  for (int k = 0; k < kDenseWarpTiles; ++k) {
+    const int r = k * 32 + lane;
+    len[k] = r < p.rows ? p.units(r) : 0;
+  }
+  long long incl[kDenseWarpTiles], total = 0;    // inclusive prefixes
+#pragma unroll
+  for (int k = 0; k < kDenseWarpTiles; ++k) {
+    incl[k] = total;
+    if (k * 32 < p.rows) {
+      long long v = len[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += u;
+      }
+      incl[k] += v;
+      total += __shfl_sync(0xffffffffu, v, 31);
+    }
+  }
+  const long long share = p.share(total), begin = pair * share;
+  DenseWalk w{0, 0, max(0ll, min(total, begin + share) - begin)};
+#pragma unroll
+  for (int k = 0; k < kDenseWarpTiles; ++k) {
+    const bool mine = incl[k] - len[k] <= begin && begin < incl[k];
+    const uint32_t hit = __ballot_sync(0xffffffffu, mine);
+    if (hit) {
+      w.row = k * 32 + __ffs(hit) - 1;
+      w.off = __shfl_sync(0xffffffffu, begin - (incl[k] - len[k]), __ffs(hit) - 1);
+    }
+  }
+  return w;
+}
+// Any number of rows: block-wide sums through `scan` (WARPS + 2 words, the last
+// two for the start); every thread calls it.
+template <int WARPS>
+__device__ __forceinline__ DenseWalk dense_share_block(const DenseParams& p, int pair, long long* scan) {
+  constexpr int THREADS = 32 * WARPS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  long long total = 0;
+  for (int r = threadIdx.x; r < p.rows; r += THREADS) total += p.units(r);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (lane == 0) scan[warp] = total;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int i = 0; i < WARPS; ++i) total += scan[i];
+  const long long share = p.share(total), begin = pair * share;
+  DenseWalk w{0, 0, max(0ll, min(total, begin + share) - begin)};
+  for (long long base = 0, r0 = 0; r0 < p.rows && w.left > 0; r0 += THREADS) {
+    // exclusive prefix of this thread's row within the tile of rows
+    const int r = static_cast<int>(r0) + threadIdx.x;
+    const int len = r < p.rows ? p.units(r) : 0;
+    long long incl = len;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    long long before = base;
+    for (int i = 0; i < WARPS; ++i) {
+      if (i < warp) before += scan[i];
+      base += scan[i];
+    }
+    const long long at = before + incl - len;
+    if (at <= begin && begin < at + len) {
+      scan[WARPS] = r;
+      scan[WARPS + 1] = begin - at;
+    }
+    if (base > begin) break;                     // the same in every thread
+  }
+  __syncthreads();
+  if (w.left > 0) {
+    w.row = static_cast<int>(scan[WARPS]);
+    w.off = scan[WARPS + 1];
+  }
+  return w;
+}
+
+// out = 0 and LSE = -inf for CTA `rank`'s heads of row r, by one warp.
+__device__ __forceinline__ void dense_empty_row(const DenseParams& p, int r, int rank, int lane) {
+  const int h0 = rank * DenseTile::HB, h1 = min(p.H, h0 + DenseTile::HB);
+  const size_t bytes = p.out_bf16 ? 1024 : 2048;
+  const size_t first = static_cast<size_t>(r) * p.H;
+  if (h0 >= h1) return;
+  uint4* o = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + (first + h0) * bytes);
+  const int n = (h1 - h0) * static_cast<int>(bytes / 16);
+  for (int i = lane; i < n; i += 32) o[i] = make_uint4(0, 0, 0, 0);
+  if (p.lse)
+    for (int h = h0 + lane; h < h1; h += 32) p.lse[first + h] = -INFINITY;
+}
+
 // tmap_kv: the cache as [9 dim blocks][rows][64], box 64 dims x 64 rows x 2
 // blocks (blocks past the ninth read as zero). tmap_q: Q as
-// [rows][H][576], box 64 dims x 64 heads. tmap_o, tmap_p: out and part_o as
-// [rows or slots][H][512 elements in bytes], box 128 bytes x 64 heads. All with
-// the 128-byte swizzle; heads past H read as zero and are not stored.
+// [rows][9 dim blocks][H][64], box 64 dims x 64 heads x 9 blocks; heads past H
+// read as zero. Both with the 128-byte swizzle.
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     dense_attn_kernel(const __grid_constant__ CUtensorMap tmap_kv,
-                      const __grid_constant__ CUtensorMap tmap_q,
-                      const __grid_constant__ CUtensorMap tmap_o,
-                      const __grid_constant__ CUtensorMap tmap_p, const DenseParams p) {
+                      const __grid_constant__ CUtensorMap tmap_q, const DenseParams p) {
   using T = DenseTile;
   constexpr int NK = T::NK;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -172,16 +269,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   uint64_t* pv_done = q_full + 8;                // O += P V finished
   uint64_t* tail = q_full + 9;                   // a partly filled V entry landed
   long long* scan = reinterpret_cast<long long*>(smem + T::OFF_SCAN);
-  int* start = reinterpret_cast<int*>(scan + 12);              // row, block of the share's begin
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(start + 2);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(scan + T::THREADS / 32 + 2);
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int pair = blockIdx.x >> 1;
   const uint32_t rank = cluster_ctarank();       // = blockIdx.x & 1
 
+  if ((smem_u32(smem_raw) & 1023u) != 0) {       // see SMEM_BYTES: no slack to realign; in both CTAs
+    if (threadIdx.x == 0) raise_error(kErrInternal);
+    return;
+  }
   if (threadIdx.x == 0) {
-    if ((smem_u32(smem_raw) & 1023u) != 0) raise_error(kErrInternal);   // see SMEM_BYTES: no slack
     for (int s = 0; s < T::RING; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&far_full[s], 1);
@@ -202,76 +301,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     prefetch_tmap(&tmap_q);
   }
   griddep_launch_dependents();                   // the join may be launched (it waits for this grid)
-  // ---- the share: blocks [begin, end) of the line of all rows' blocks
-  constexpr int kWarps = T::THREADS / 32;
-  long long mine = 0;
-  for (int r = threadIdx.x; r < p.rows; r += T::THREADS) mine += p.blocks(r);
-  const long long total = dense_block_sum<kWarps>(mine, scan);
-  const long long share = p.share(total);
-  const long long begin = pair * share;
-  DenseWalk walk{0, 0, max(0ll, min(total, begin + share) - begin)};
-  // the same in every thread of both CTAs: no TMEM, no copies yet
-  if (walk.left == 0 || (smem_u32(smem_raw) & 1023u) != 0) return;
-  for (long long base = 0, r0 = 0; r0 < p.rows; r0 += T::THREADS) {
-    // exclusive prefix of this thread's row within the tile of rows
-    const int r = static_cast<int>(r0) + threadIdx.x;
-    const int nb = r < p.rows ? p.blocks(r) : 0;
-    long long incl = nb;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = base;
-    for (int i = 0; i < kWarps; ++i) {
-      if (i < warp) before += scan[i];
-      base += scan[i];
-    }
-    const long long at = before + incl - nb;
-    if (nb > 0 && at <= begin && begin < at + nb) {
-      start[0] = r;
-      start[1] = static_cast<int>(begin - at);
-    }
-    if (base > begin) break;                     // the same in every thread
-  }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, T::TMEM_COLS);
     tmem_relinquish_pair();
   }
+  DenseWalk walk = p.rows <= 32 * kDenseWarpTiles ? dense_share_warp(p, pair)
+                                                 : dense_share_block<T::THREADS / 32>(p, pair, scan);
   tc_fence_before();
   cluster_sync();                                // also: both CTAs' barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
-  walk.row = start[0];
-  walk.blk = start[1];
 
   // Every role walks the same segments and counts alike: g is the pair's
-  // running block number, e the running ring entry. In a segment of n blocks
-  // the entries are those of S(0), S(1), V(0), S(2), V(1), ..., V(n - 1).
+  // running block number, es and ev the rings' running entries. A segment of n
+  // blocks is computed as S(0), S(1), V(0), S(2), V(1), ..., V(n - 1).
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ loads
-    // Warp 0 loads Q and the S entries, warp 2 the V entries: issuing a copy
-    // takes one thread about 290 cycles, nine of them would bound a block.
-    // Both walk every entry and wait until it is free, so that a barrier is
-    // never two phases ahead of a waiting thread.
+    // Warp 0 loads Q and the S ring, warp 2 the V ring: issuing a copy takes one
+    // thread about 290 cycles, nine of them would bound a block. A ring has one
+    // loader, which waits for every entry of it in turn, so no barrier is ever
+    // more than a phase away from a waiting thread.
     const bool for_s = warp == 0;
-    uint32_t e = 0, segs = 0, tails = 0;
-    uint32_t mine = 0, phase = 0;                // slots this warp has filled, and their phases
+    uint32_t e = 0, segs = 0, tails = 0;         // e: entries of this warp's ring
     bool ok = true;
     DenseSeg w;
-    // One entry: waits until its slot is free and returns it.
-    auto slot_free = [&]() -> uint32_t {
-      const uint32_t st = e % T::RING;
-      ok = mbar_wait(&empty[st], ((e / T::RING) & 1) ^ 1);
-      return st;
-    };
-    auto filled = [&](uint32_t st) {
-      mine |= 1u << st;
-      phase = (phase & ~(1u << st)) | (((e / T::RING) & 1) << st);
-    };
     while (ok && walk.next(p, w)) {
       const int b = w.row / p.n_q;
       // The pool row of a block's first key: a block of 128 lies inside one
@@ -280,81 +333,79 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         const int64_t r = p.km.row(b, blk * NK, p.n_kv);
         return static_cast<int>(r >= 0 ? r : p.km.pool_rows);
       };
+      int y = locate(w.blk);
       if (for_s) {
         // Q of this CTA's heads, once the previous segment's last S has read it
         if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_full, T::QB * T::BOX);
-          for (int t = 0; t < T::QB; ++t)
-            tma_load_3d(q_smem + t * T::BOX, &tmap_q, q_full, t * 64, static_cast<int>(rank) * T::HB, w.row);
+          tma_load_4d(q_smem, &tmap_q, q_full, 0, static_cast<int>(rank) * T::HB, 0, w.row);
         }
-      }
-      ++segs;
-      int y = locate(w.blk);                     // of the block this warp loads next
-      for (int i = 0; i <= w.n && ok; ++i) {
-        if (i < w.n) {
+        ++segs;
+        for (int i = 0; i < w.n && ok; ++i) {
           // S(i): this CTA's 64 keys, dims 128 t .. + 127 (the last entry: 64)
           for (int t = 0; t < T::SE; ++t, ++e) {
-            const uint32_t st = slot_free();
+            const uint32_t st = e % T::RS;
+            ok = mbar_wait(&empty[st], ((e / T::RS) & 1) ^ 1);
             if (!ok) break;
-            if (!for_s) continue;
-            filled(st);
             if (lane == 0) {
               mbar_arrive_expect_tx(&full[st], T::ENTRY);
               tma_load_3d(ring + st * T::ENTRY, &tmap_kv, &full[st], 0, y + static_cast<int>(rank) * 64, 2 * t);
             }
           }
-          if (!ok) break;
-          if (for_s && i + 1 < w.n) y = locate(w.blk + i + 1);
+          if (i + 1 < w.n) y = locate(w.blk + i + 1);
         }
-        if (i == 0) continue;
-        // V(i - 1): entry (key half kh, accumulator j): dims 256 j + 128 rank .. + 127
-        const int valid = w.vis - (w.blk + i - 1) * NK;
-        for (int t = 0; t < T::VE; ++t, ++e) {
-          const uint32_t st = slot_free();
-          if (!ok) break;
-          if (for_s) continue;
-          filled(st);
-          const int kh = t >> 1, zb = 4 * (t & 1) + 2 * static_cast<int>(rank);
-          const int rows = valid - 64 * kh;      // of this half that hold keys
-          uint8_t* dst = ring + st * T::ENTRY;
-          if (rows >= 64 || rows <= 0) {
-            // a half without keys reads as zeros: past the end of the pool
-            if (lane == 0) {
-              mbar_arrive_expect_tx(&full[st], T::ENTRY);
-              tma_load_3d(dst, &tmap_kv, &full[st], 0, rows > 0 ? y + 64 * kh : static_cast<int>(p.km.pool_rows), zb);
+      } else {
+        for (int i = 0; i < w.n && ok; ++i) {
+          // V(i): entry (key half kh, accumulator j): dims 256 j + 128 rank .. + 127
+          const int valid = w.vis - (w.blk + i) * NK;
+          for (int t = 0; t < T::VE; ++t, ++e) {
+            const uint32_t st = T::RS + e % T::RV;
+            ok = mbar_wait(&empty[st], ((e / T::RV) & 1) ^ 1);
+            if (!ok) break;
+            const int kh = t >> 1, zb = 4 * (t & 1) + 2 * static_cast<int>(rank);
+            const int rows = valid - 64 * kh;    // of this half that hold keys
+            uint8_t* dst = ring + st * T::ENTRY;
+            if (rows >= 64 || rows <= 0) {
+              // a half without keys reads as zeros: past the end of the pool
+              if (lane == 0) {
+                mbar_arrive_expect_tx(&full[st], T::ENTRY);
+                tma_load_3d(dst, &tmap_kv, &full[st], 0,
+                            rows > 0 ? y + 64 * kh : static_cast<int>(p.km.pool_rows), zb);
+              }
+            } else {
+              if (lane == 0) {
+                mbar_arrive_expect_tx(tail, T::ENTRY);
+                tma_load_3d(dst, &tmap_kv, tail, 0, y + 64 * kh, zb);
+              }
+              ok = mbar_wait(tail, tails & 1) || mbar_wait(tail, tails & 1);
+              ++tails;
+              for (int k = lane; k < (64 - rows) * 8; k += 32) {
+                sts_v4(smem_u32(dst) + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
+                sts_v4(smem_u32(dst) + T::BOX + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&full[st]);
             }
-          } else {
-            if (lane == 0) {
-              mbar_arrive_expect_tx(tail, T::ENTRY);
-              tma_load_3d(dst, &tmap_kv, tail, 0, y + 64 * kh, zb);
-            }
-            ok = mbar_wait(tail, tails & 1) || mbar_wait(tail, tails & 1);
-            ++tails;
-            for (int k = lane; k < (64 - rows) * 8; k += 32) {
-              sts_v4(smem_u32(dst) + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
-              sts_v4(smem_u32(dst) + T::BOX + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[st]);
           }
+          if (i + 1 < w.n) y = locate(w.blk + i + 1);
         }
-        if (!for_s && i < w.n) y = locate(w.blk + i);
       }
       __syncwarp();
     }
     // A wait that ran out leaves copies in flight: they end before the CTA does.
     if (!ok) {
-      for (uint32_t st = 0; st < T::RING; ++st)
-        if ((mine >> st) & 1u) mbar_wait(&full[st], (phase >> st) & 1u);
+      const uint32_t n = for_s ? T::RS : T::RV;
+      for (uint32_t d = 1; d <= n && d <= e; ++d)
+        mbar_wait(&full[(for_s ? 0 : T::RS) + (e - d) % n], ((e - d) / n) & 1);
       if (for_s && segs > 0) mbar_wait(q_full, (segs - 1) & 1);
     }
   } else if (warp == 1 && rank == 1) {
     // ------------------------------------------------------------ arrivals passed on to CTA 0
     if (elect_one()) {
-      uint32_t e = 0, segs = 0;
+      uint32_t es = 0, ev = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
       while (ok && walk.next(p, w)) {
@@ -362,11 +413,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (!ok) break;
         mbar_arrive_at(far_q, 0);
         ++segs;
-        const uint32_t last = e + static_cast<uint32_t>(w.n) * (T::SE + T::VE);
-        for (; e < last; ++e) {
-          ok = mbar_wait(&full[e % T::RING], (e / T::RING) & 1);
-          if (!ok) break;
-          mbar_arrive_at(&far_full[e % T::RING], 0);
+        for (int i = 0; i <= w.n && ok; ++i) {   // in the order the MMAs read
+          for (int t = 0; t < T::SE && i < w.n && ok; ++t, ++es) {
+            ok = mbar_wait(&full[es % T::RS], (es / T::RS) & 1);
+            if (ok) mbar_arrive_at(&far_full[es % T::RS], 0);
+          }
+          for (int t = 0; t < T::VE && i > 0 && ok; ++t, ++ev) {
+            const uint32_t st = T::RS + ev % T::RV;
+            ok = mbar_wait(&full[st], (ev / T::RV) & 1);
+            if (ok) mbar_arrive_at(&far_full[st], 0);
+          }
         }
       }
     }
@@ -380,11 +436,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const uint64_t v_desc0 = umma_desc(smem_u32(ring), T::BOX, 1024, 2);
       const uint64_t q_desc0 = umma_desc(smem_u32(q_smem), 16, 1024, 2);
       const uint64_t p_desc0 = umma_desc(smem_u32(smem + T::OFF_P), 16, 1024, 2);
-      uint32_t e = 0, g = 0, segs = 0;
+      uint32_t es = 0, ev = 0, g = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
-      auto landed = [&]() {
-        const uint32_t st = e % T::RING, ph = (e / T::RING) & 1;
+      auto landed = [&](uint32_t st, uint32_t ph) {
         ok = mbar_wait(&full[st], ph) && mbar_wait(&far_full[st], ph);
         tc_fence_after();
         return ok;
@@ -402,16 +457,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             const uint32_t d = tmem_base + T::COL_S + b * 64;
 #pragma unroll
             for (int t = 0; t < T::SE; ++t) {
-              if (!landed()) break;
-              const uint64_t kd = k_desc0 + static_cast<uint32_t>((e % T::RING) * (T::ENTRY >> 4));
+              const uint32_t st = es % T::RS;
+              if (!landed(st, (es / T::RS) & 1)) break;
+              const uint64_t kd = k_desc0 + static_cast<uint32_t>(st * (T::ENTRY >> 4));
 #pragma unroll
               for (int kk = 0; kk < (t < 4 ? 8 : 4); ++kk) {
                 const uint32_t off = ((kk >> 2) * T::BOX + (kk & 3) * 32) >> 4;
                 umma_bf16_ss_pair(d, q_desc0 + (t * (T::ENTRY >> 4) + off), kd + off, idesc_s,
                                   (t | kk) ? 1u : 0u);
               }
-              umma_commit_pair(&empty[e % T::RING]);
-              ++e;
+              umma_commit_pair(&empty[st]);
+              ++es;
             }
             if (!ok) break;
             umma_commit_pair(&s_full[b]);
@@ -425,15 +481,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const uint32_t more_o = i > 1 ? 1u : 0u;   // a segment's first product overwrites O
 #pragma unroll
           for (int t = 0; t < T::VE; ++t) {
-            if (!landed()) break;
-            const uint64_t vd = v_desc0 + static_cast<uint32_t>((e % T::RING) * (T::ENTRY >> 4));
+            const uint32_t st = T::RS + ev % T::RV;
+            if (!landed(st, (ev / T::RV) & 1)) break;
+            const uint64_t vd = v_desc0 + static_cast<uint32_t>(st * (T::ENTRY >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_bf16_ss_pair(tmem_base + T::COL_O + (t & 1) * 128,
                                 p_desc0 + (((t >> 1) * T::BOX + kk * 32) >> 4), vd + ((kk * 2048) >> 4),
                                 idesc_pv, (t > 1 || kk > 0) ? 1u : more_o);
-            umma_commit_pair(&empty[e % T::RING]);
-            ++e;
+            umma_commit_pair(&empty[st]);
+            ++ev;
           }
           if (ok) umma_commit_pair(pv_done);
         }
@@ -441,6 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ the cut; rows that see no key
+    DenseSeg w;
+    const bool any = walk.next(p, w);
+    if (lane == 0 && rank == 0) p.cut[pair] = any ? make_int2(w.row, w.blk) : make_int2(-1, 0);
+    for (int r = pair; r < p.rows; r += p.pairs)
+      if (p.blocks(r) == 0) dense_empty_row(p, r, static_cast<int>(rank), lane);
   } else if (warp >= T::SM0) {
     // ------------------------------------------------------------ softmax / epilogue
     const int quarter = warp & 3;
@@ -451,7 +515,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     const uint32_t lane_addr = static_cast<uint32_t>(quarter * 32) << 16;
     const uint32_t head_bar = 1u + static_cast<uint32_t>(quarter & 1);   // the four warps of its heads
     float* red = reinterpret_cast<float*>(smem + T::OFF_RED);   // [parity][part][64]
-    const int stid = threadIdx.x - T::SM0 * 32;              // 0..255 over the softmax warps
     constexpr uint32_t kAllBar = 5u;                         // named barrier of the 8 warps
     constexpr uint32_t kAllThreads = 32u * T::SOFTMAX_WARPS;
     const int head = static_cast<int>(rank) * T::HB + h;     // of the row
@@ -566,94 +629,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       red[part * T::HB + h] = l;
       red[(4 + part) * T::HB + h] = l_mma;
       const bool pv_ok = named_bar_and(kAllBar, kAllThreads, ok);
-      float l_all = 0.f, lm_all = 0.f;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        l_all += red[k * T::HB + h];
-        lm_all += red[(4 + k) * T::HB + h];
-      }
-      named_bar_sync(kAllBar, kAllThreads);      // read before the next segment's maxima
       // O / sum(rounded p) is an exact convex combination of the V rows; the
-      // LSE keeps the unrounded sum.
-      const bool has = pv_ok && l_all != 0.f && lm_all != 0.f;   // true for NaN
-      const float inv_l = has ? 1.0f / lm_all : 0.f;
-      const uint32_t keep = has ? 0xffffffffu : 0u;
-      const float lse_v = has ? (m_used + log2f(l_all)) * 0.69314718055994531f : -INFINITY;
-      // O leaves by TMA stores of 128-byte-wide column slices of the 64 heads,
-      // staged in the swizzled layout the store reads. A round covers the
-      // same slice of both lane halves (dims 128 apart): through the P area (free: the
-      // last PV has finished), one round at a time; after the last segment
-      // every round at once through the ring.
+      // LSE keeps the unrounded sum. O goes straight from TMEM to memory: in the
+      // 16x256b shape four lanes hold 8 neighbouring columns of a row, a full
+      // sector of fp32 per row and store. (Staged through shared memory for TMA
+      // stores it took 2 us at the end of a share and 5 us between two rows.)
       const bool direct = done.whole;
       const int slot = 2 * pair + (done.blk > 0 ? 0 : 1);
       const bool bf16_out = direct && p.out_bf16;
-      const int esz = bf16_out ? 2 : 4;
-      const int cols = 128 / esz;                // of a slice
-      const int rounds = 256 / cols;             // slices of a lane's 256 columns
-      const int per_step = more ? 1 : rounds;
-      const int z0 = direct ? done.row : slot;
+      const size_t out_row = static_cast<size_t>(direct ? done.row : slot) * p.H;
 #pragma unroll 1
-      for (int r0 = 0; r0 < rounds; r0 += per_step) {
-        const uint32_t stage = more ? smem_u32(smem + T::OFF_P) : smem_u32(ring);
-        if (r0 > 0 && stid == 0) bulk_wait_read<0>();    // the last step's stores have read it
-        if (r0 > 0) named_bar_sync(kAllBar, kAllThreads);
-        for (int r = r0; r < r0 + per_step; ++r) {
-          const uint32_t srow = stage + ((r - r0) * 2 + side) * T::BOX + h * 128;
-#pragma unroll 1
-          for (int c = half * (cols / 2); c < (half + 1) * (cols / 2); c += 16) {
-            uint32_t o[16];
-            tmem_ld16(tmem_base + lane_addr + T::COL_O + r * cols + c, o);
-            tmem_wait_ld();
+      for (int rb = 0; rb < 2; ++rb) {
+        // this thread's two heads of the 16 lanes
+        float inv[2];
+        size_t at[2];
+        bool there[2];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j] & keep) * inv_l);
-            const int cc = c * esz / 16;                   // its first 16-byte chunk in the row
-            if (bf16_out) {
-              uint32_t pkd[8];
+        for (int k = 0; k < 2; ++k) {
+          const int hh = (quarter & 1) * 32 + rb * 16 + 8 * k + (lane >> 2);
+          float lm = 0.f;
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 v =
-                    __floats2bfloat162_rn(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
-                pkd[j] = *reinterpret_cast<const uint32_t*>(&v);
-              }
-#pragma unroll
-              for (int q2 = 0; q2 < 2; ++q2)
-                sts_v4(srow + (((cc + q2) ^ (h & 7)) << 4), pkd[4 * q2], pkd[4 * q2 + 1],
-                       pkd[4 * q2 + 2], pkd[4 * q2 + 3]);
-            } else {
-#pragma unroll
-              for (int q2 = 0; q2 < 4; ++q2)
-                sts_v4(srow + (((cc + q2) ^ (h & 7)) << 4), o[4 * q2], o[4 * q2 + 1], o[4 * q2 + 2],
-                       o[4 * q2 + 3]);
-            }
-          }
+          for (int q = 0; q < 4; ++q) lm += red[(4 + q) * T::HB + hh];
+          inv[k] = pv_ok && lm != 0.f ? 1.0f / lm : 0.f;                 // NaN goes through
+          const int hd = static_cast<int>(rank) * T::HB + hh;
+          there[k] = hd < p.H;
+          at[k] = (out_row + hd) * T::DV + half * 256 + side * 128 + (lane & 3) * 2;
         }
-        fence_proxy_async_smem();
-        named_bar_sync(kAllBar, kAllThreads);
-        if (stid == 0 && static_cast<int>(rank) * T::HB < p.H) {
-          const void* map = direct ? static_cast<const void*>(&tmap_o) : static_cast<const void*>(&tmap_p);
-          for (int r = r0; r < r0 + per_step; ++r)
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t o[16];
+          tmem_ld_16x256b_x4(tmem_base + lane_addr + (static_cast<uint32_t>(rb * 16) << 16) + T::COL_O +
+                                 half * 128 + c, o);
+          tmem_wait_ld();
 #pragma unroll
-            for (int sd = 0; sd < 2; ++sd) {
-              // lane half sd of columns [r cols, + cols): accumulator j = column / 128
-              const int col = r * cols;
-              const int dim = (col >> 7) * 256 + sd * 128 + (col & 127);
-              tma_store_3d(map, stage + ((r - r0) * 2 + sd) * T::BOX, dim * esz,
-                           static_cast<int>(rank) * T::HB, z0);
+          for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if (!there[k]) continue;
+              const float x = inv[k] == 0.f ? 0.f : __uint_as_float(o[4 * b + 2 * k]) * inv[k];
+              const float y = inv[k] == 0.f ? 0.f : __uint_as_float(o[4 * b + 2 * k + 1]) * inv[k];
+              const size_t e = at[k] + c + 8 * b;
+              if (bf16_out) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+                *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + e) = v;
+              } else {
+                float* dst = direct ? static_cast<float*>(p.out) : p.part_o;
+                *reinterpret_cast<float2*>(dst + e) = make_float2(x, y);
+              }
             }
-          bulk_commit();
         }
       }
-      // every staged byte read before the next segment writes P
-      if (stid == 0) bulk_wait_read<0>();
       if (part == 0 && head < p.H) {
+        float l_all = 0.f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) l_all += red[k * T::HB + h];
+        const float lse_v = pv_ok && l_all != 0.f ? (m_used + log2f(l_all)) * 0.69314718055994531f : -INFINITY;
         if (!direct) p.part_lse[static_cast<size_t>(slot) * p.H + head] = lse_v;
         else if (p.lse) p.lse[static_cast<size_t>(done.row) * p.H + head] = lse_v;
       }
+      tc_fence_before();
+      // red and O read before the next segment's maxima and its first P V
       ok = named_bar_and(kAllBar, kAllThreads, ok);
     }
   }
 
-  if (threadIdx.x == T::SM0 * 32) bulk_wait<0>();   // the output stores have completed
   tc_fence_before();
   __syncwarp();
   cluster_sync();                                // no arrival or MMA of the pair is outstanding
@@ -663,110 +702,134 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   }
 }
 
-// Joins the partials of the rows that more than one share holds, in key order,
-// and writes the rows that see no key (out = 0, LSE = -inf). G warps per (row,
-// head) take every G-th partial, a lane 16 of the 512 value dims; their sums
-// meet in shared memory. The shares are derived as the attention kernel derives
-// them. Few rows may have a partial from every pair (one long sequence: 74 of
-// them), so they get more warps: 36 -> 8 us with G = 8 against one thread
-// walking all partials.
-template <int G>
+constexpr int kDenseMaxPairs = 128;
+
+// Joins the partials of the rows that more than one share holds, in key order.
+// blockIdx.x counts those rows: row k is the k-th whose beginning lies in a
+// share that does not hold its end. A head's 512 value dims go to 512 / (32 VW)
+// warps with VW dims per lane. Few rows may have a partial from every pair (one
+// long sequence: 74 of them), so they get eight warps a head (VW = 2), many
+// rows one (VW = 16). No shared memory: the attention kernel leaves none for a
+// CTA that waits beside it.
+template <int VW>
 __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseParams p) {
-  constexpr int HEADS = 8 / G;                   // heads per CTA
-  __shared__ longlong2 scan[8];
-  __shared__ float4 acc_s[G > 1 ? 8 : 1][4][32];
-  __shared__ float sum_s[8];
+  constexpr int WPH = 512 / (32 * VW);           // warps per head
+  constexpr int V = VW < 4 ? VW : 4;             // dims per load
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = blockIdx.x;
-  const int h = blockIdx.y * HEADS + warp / G, sub = warp % G;
-  long long total = 0, first = 0;                // blocks of all rows, of the rows ahead
-  for (int r = threadIdx.x; r < p.rows; r += 256) {
-    const int nb = p.blocks(r);
-    total += nb;
-    if (r < row) first += nb;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    first += __shfl_xor_sync(0xffffffffu, first, o);
-  }
-  if (lane == 0) scan[warp] = make_longlong2(total, first);
-  __syncthreads();
-  total = first = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    total += scan[i].x;
-    first += scan[i].y;
-  }
-  const int nb = p.blocks(row);
-  const long long share = p.share(total);
-  const int p0 = static_cast<int>(first / share);
-  const int np = nb > 0 ? static_cast<int>((first + nb - 1) / share) - p0 + 1 : 0;
+  const int h = blockIdx.y * (8 / WPH) + warp / WPH;
+  const int dim0 = (warp % WPH) * 32 * VW;
+  constexpr int K = kDenseMaxPairs / 32;
   griddep_wait();                                // every CTA: this grid ends after the attention
-  if (np == 1) return;                           // written by the attention kernel
-  // the row begins in share p0 (slot 2 p0 + 1); the others begin inside of it
+  // the cuts, lane q % 32 of word q / 32 for share q. `inside`: the share begins
+  // inside a row; `opens`: and the row begins in the share before
+  int2 c[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int q = k * 32 + lane;
+    c[k] = q < p.pairs ? p.cut[q] : make_int2(-1, 0);
+  }
+  int found = -1, row = 0, seen = 0, np = 1;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    int2 b = make_int2(__shfl_up_sync(0xffffffffu, c[k].x, 1), __shfl_up_sync(0xffffffffu, c[k].y, 1));
+    if (k > 0) {
+      const int bx = __shfl_sync(0xffffffffu, c[k > 0 ? k - 1 : 0].x, 31);
+      const int by = __shfl_sync(0xffffffffu, c[k > 0 ? k - 1 : 0].y, 31);
+      if (lane == 0) b = make_int2(bx, by);
+    }
+    const bool inside = c[k].x >= 0 && c[k].y > 0;     // never so for share 0
+    const uint32_t opens = __ballot_sync(0xffffffffu, inside && !(b.y > 0 && b.x == c[k].x));
+    if (found < 0) {
+      const int nth = static_cast<int>(blockIdx.x) - seen;
+      seen += __popc(opens);
+      if (nth < __popc(opens)) {
+        const bool is_nth = ((opens >> lane) & 1u) && __popc(opens & ((1u << lane) - 1u)) == nth;
+        const int bit = __ffs(__ballot_sync(0xffffffffu, is_nth)) - 1;
+        found = k * 32 + bit - 1;                // the share the row begins in
+        row = __shfl_sync(0xffffffffu, c[k].x, bit);
+      }
+    }
+    // a row's shares follow one another, so counting them all is counting its own
+    if (found >= 0) np += __popc(__ballot_sync(0xffffffffu, inside && c[k].x == row));
+  }
+  if (found < 0 || h >= p.H) return;
+  // the row begins in share `found` (slot 2 found + 1); the others begin inside of it
   auto slot = [&](int i) {
-    return (static_cast<size_t>(2 * (p0 + i)) + (i == 0 ? 1 : 0)) * p.H + h;
+    return (static_cast<size_t>(2 * (found + i)) + (i == 0 ? 1 : 0)) * p.H + h;
   };
-  const bool there = h < p.H;
+  float w[K];                                    // LSE, then weight, of partial 32 k + lane
   float m = -INFINITY;
-  if (there)
-    for (int i = lane; i < np; i += 32) m = fmaxf(m, p.part_lse[slot(i)]);
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    w[k] = k * 32 + lane < np ? p.part_lse[slot(k * 32 + lane)] : -INFINITY;
+    m = fmaxf(m, w[k]);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  float4 acc[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f;
-  if (there) {
-#pragma unroll 2
-    for (int i = sub; i < np; i += G) {
-      const size_t at = slot(i);
-      const float ls = p.part_lse[at];
-      const float wgt = ls == -INFINITY ? 0.f : __expf(ls - m);
-      sum += wgt;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * 512 + j * 128 + lane * 4);
-        acc[j].x = fmaf(wgt, v.x, acc[j].x);
-        acc[j].y = fmaf(wgt, v.y, acc[j].y);
-        acc[j].z = fmaf(wgt, v.z, acc[j].z);
-        acc[j].w = fmaf(wgt, v.w, acc[j].w);
+  for (int k = 0; k < K; ++k) {
+    w[k] = w[k] == -INFINITY ? 0.f : __expf(w[k] - m);
+    sum += w[k];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  float acc[VW];
+#pragma unroll
+  for (int j = 0; j < VW; ++j) acc[j] = 0.f;
+  constexpr int UN = VW <= 2 ? 16 : 2;           // partials loaded before the first is added
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    const int n = min(32, np - k * 32);
+    for (int i0 = 0; i0 < n; i0 += UN) {
+      float v[UN][VW];
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const bool on = i0 + u < n;
+        const float* src = p.part_o + slot(k * 32 + i0 + u) * 512 + dim0 + lane * V;
+#pragma unroll
+        for (int j = 0; j < VW; j += V) {
+          if constexpr (V == 4) {
+            const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(src + j * 32)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[u][j] = t.x; v[u][j + 1] = t.y; v[u][j + 2] = t.z; v[u][j + 3] = t.w;
+          } else {
+            const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(src + j * 32)) : make_float2(0.f, 0.f);
+            v[u][j] = t.x; v[u][j + 1] = t.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < UN; ++u) {
+        const float wgt = __shfl_sync(0xffffffffu, w[k], (i0 + u) & 31);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) acc[j] = fmaf(wgt, v[u][j], acc[j]);
       }
     }
   }
-  if constexpr (G > 1) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc_s[warp][j][lane] = acc[j];
-    if (lane == 0) sum_s[warp] = sum;
-    __syncthreads();
-    if (sub != 0) return;
-#pragma unroll
-    for (int k = 1; k < G; ++k) {
-      sum += sum_s[warp + k];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 v = acc_s[warp + k][j][lane];
-        acc[j].x += v.x; acc[j].y += v.y; acc[j].z += v.z; acc[j].w += v.w;
-      }
-    }
-  }
-  if (!there) return;
   const float inv = sum != 0.f ? 1.0f / sum : 0.f;     // NaN goes through
-  const size_t o = (static_cast<size_t>(row) * p.H + h) * 512;
+  const size_t o = (static_cast<size_t>(row) * p.H + h) * 512 + dim0;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 v = make_float4(acc[j].x * inv, acc[j].y * inv, acc[j].z * inv, acc[j].w * inv);
-    const size_t at = o + j * 128 + lane * 4;
+  for (int j = 0; j < VW; j += V) {
+    const size_t at = o + (j / V) * 32 * V + lane * V;
     if (p.out_bf16) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      uint32_t w[V / 2];
+#pragma unroll
+      for (int k = 0; k < V / 2; ++k) {
+        const __nv_bfloat162 t = __floats2bfloat162_rn(acc[j + 2 * k] * inv, acc[j + 2 * k + 1] * inv);
+        w[k] = *reinterpret_cast<const uint32_t*>(&t);
+      }
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.out) + at);
+      if constexpr (V == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else *dst = w[0];
     } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = v;
+      float* dst = static_cast<float*>(p.out) + at;
+      if constexpr (V == 4)
+        *reinterpret_cast<float4*>(dst) =
+            make_float4(acc[j] * inv, acc[j + 1] * inv, acc[j + 2] * inv, acc[j + 3] * inv);
+      else *reinterpret_cast<float2*>(dst) = make_float2(acc[j] * inv, acc[j + 1] * inv);
     }
   }
-  if (lane == 0 && p.lse)
+  if (dim0 == 0 && lane == 0 && p.lse)
     p.lse[static_cast<size_t>(row) * p.H + h] = sum != 0.f ? m + logf(sum) : -INFINITY;
 }
 

@@ -734,40 +734,36 @@ dsa_status check_dense_shape(const dsa_shape* s) {
   return DSA_OK;
 }
 
-// Two partial rows (O fp32, LSE) per CTA pair: those that its share's ends cut.
+// Two partial rows (O fp32, LSE) per CTA pair: those that its share's ends cut;
+// and where each share begins.
 struct DensePlan {
   int pairs;
-  size_t o_bytes, total;
+  size_t o_bytes, lse_bytes, total;
 };
 DensePlan plan_dense(const dsa_shape* s) {
   DensePlan d{};
-  d.pairs = std::max(1, num_sms() / 2);
+  d.pairs = std::max(1, std::min(num_sms() / 2, dsa::kDenseMaxPairs));
   const size_t rows = 2 * static_cast<size_t>(d.pairs) * s->heads;
   d.o_bytes = (rows * s->v_dim * sizeof(float) + 255) / 256 * 256;
-  d.total = d.o_bytes + (rows * sizeof(float) + 255) / 256 * 256;
+  d.lse_bytes = (rows * sizeof(float) + 255) / 256 * 256;
+  d.total = d.o_bytes + d.lse_bytes + (d.pairs * sizeof(int2) + 255) / 256 * 256;
   return d;
 }
 
-// A 3D tensor for the dense attention's TMA copies: 128-byte swizzle, a box of
-// 128 bytes x 64 rows x depth. dims and strides (bytes, of dims 1..) as
+// A bf16 tensor for the dense attention's TMA loads: 128-byte swizzle, a box of
+// 64 dims x 64 rows x depth (x 1). dims and strides (bytes, of dims 1..) as
 // cuTensorMapEncodeTiled takes them.
-dsa_status make_tmap_dense(CUtensorMap* map, CUtensorMapDataType type, const void* base,
-                           const cuuint64_t (&dims)[3], const cuuint64_t (&strides)[2], uint32_t depth) {
+dsa_status make_tmap_dense(CUtensorMap* map, int rank, const void* base, const cuuint64_t* dims,
+                           const cuuint64_t* strides, uint32_t depth) {
   EncodeTiledFn fn = get_encode_fn();
   if (!fn) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-  const cuuint32_t box[3] = {type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 128u : 64u, 64, depth};
-  const cuuint32_t estr[3] = {1, 1, 1};
-  CUresult r = fn(map, type, 3, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t box[4] = {64, 64, depth, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(DSA_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", (int)r);
   return DSA_OK;
-}
-// [rows][heads][width bytes]
-dsa_status make_tmap_heads(CUtensorMap* map, const void* base, uint64_t rows, uint32_t heads, uint32_t width) {
-  const cuuint64_t dims[3] = {width, heads, rows};
-  const cuuint64_t strides[2] = {width, static_cast<cuuint64_t>(width) * heads};
-  return make_tmap_dense(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, base, dims, strides, 1);
 }
 
 dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_t* q,
@@ -785,32 +781,29 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   p.lse = lse;
   p.part_o = static_cast<float*>(ws);
   p.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + pl.o_bytes);
+  p.cut = reinterpret_cast<int2*>(static_cast<char*>(ws) + pl.o_bytes + pl.lse_bytes);
   p.rows = s->batch * s->n_q;
   p.n_q = s->n_q;
   p.n_kv = s->n_kv;
   p.H = s->heads;
   p.out_bf16 = out_bf16;
   p.pairs = pl.pairs;
-  p.min_share = 1;
   p.scale_log2 = s->softmax_scale * 1.4426950408889634f;
-  CUtensorMap tkv, tq, to, tp;
+  CUtensorMap tkv, tq;
   const cuuint64_t kv_dims[3] = {64, static_cast<cuuint64_t>(lay.km.pool_rows), 9}, kv_strides[2] = {1152, 128};
-  const cuuint64_t q_dims[3] = {576, static_cast<cuuint64_t>(p.H), static_cast<cuuint64_t>(p.rows)};
-  const cuuint64_t q_strides[2] = {1152, 1152ull * p.H};
-  if (dsa_status st = make_tmap_dense(&tkv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, kv, kv_dims, kv_strides, 2))
+  const cuuint64_t q_dims[4] = {64, static_cast<cuuint64_t>(p.H), 9, static_cast<cuuint64_t>(p.rows)};
+  const cuuint64_t q_strides[3] = {1152, 128, 1152ull * p.H};
+  if (dsa_status st = make_tmap_dense(&tkv, 3, kv, kv_dims, kv_strides, 2))
     return st;
-  if (dsa_status st = make_tmap_dense(&tq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q, q_dims, q_strides, 1))
+  if (dsa_status st = make_tmap_dense(&tq, 4, q, q_dims, q_strides, 9))
     return st;
-  if (dsa_status st = make_tmap_heads(&to, out, p.rows, p.H, 512 * (out_bf16 ? 2 : 4))) return st;
-  if (dsa_status st = make_tmap_heads(&tp, p.part_o, 2ull * pl.pairs, p.H, 512 * 4)) return st;
-  dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, tq, to, tp, p);
+  dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, tq, p);
   DSA_CUDA_TRY(cudaGetLastError(), "dense attention launch");
-  // the fewer rows, the more partials a row may have
-  const int g = p.rows <= 8 ? 8 : (p.rows <= 32 ? 4 : 2);
-  const dim3 jgrid(p.rows, (p.H * g + 7) / 8);
-  DSA_CUDA_TRY(g == 8   ? launch_dependent(dsa::dense_combine_kernel<8>, jgrid, dim3(256), 0, stream, p)
-               : g == 4 ? launch_dependent(dsa::dense_combine_kernel<4>, jgrid, dim3(256), 0, stream, p)
-                        : launch_dependent(dsa::dense_combine_kernel<2>, jgrid, dim3(256), 0, stream, p),
+  // the fewer rows, the more partials a row may have; at most pairs - 1 rows are cut
+  const bool few = p.rows <= 8;
+  const dim3 jgrid(std::max(1, std::min(p.rows, p.pairs - 1)), few ? p.H : (p.H + 7) / 8);
+  DSA_CUDA_TRY(few ? launch_dependent(dsa::dense_combine_kernel<2>, jgrid, dim3(256), 0, stream, p)
+                   : launch_dependent(dsa::dense_combine_kernel<16>, jgrid, dim3(256), 0, stream, p),
                "dense attention join launch");
   return DSA_OK;
 }
