@@ -33,10 +33,12 @@
 // first half of the N columns of rows 0-63, lanes 64-127 the second half): O
 // 256 columns (two N = 256 accumulators), S 2 x 64.
 //
-// Key blocks stream through two rings of 16 KB entries, one TMA copy each: S(i)
-// as five entries (64 keys x 128 dims, the last one 64), V(i) as four (64 keys x
-// 128 dims). V is loaded a second time (from L2) rather than kept from S: held
-// back until its P exists it would leave no room to load ahead.
+// Key blocks stream through one ring of 16 KB entries, one TMA copy each, in the
+// order the MMAs read them: S(i + 1) as five entries (64 keys x 128 dims, the
+// last one 64), then V(i) as four (64 keys x 128 dims). V is loaded a second time
+// (from L2) rather than kept from S: held back until its P exists it would
+// leave no room to load ahead. (A ring of four entries for each of the two:
+// 0.60 ms where the shared ring takes 0.49.)
 //
 // Rows behind a sequence's last key may hold anything, NaN and infinities too:
 // their logits are masked by selection, and the producer overwrites them with
@@ -95,8 +97,7 @@ struct DenseTile {
   static constexpr int QB = DQK / 64;           // 9 dim blocks of Q
   static constexpr int BOX = 64 * 128;          // 64 rows x 64 dims
   static constexpr int ENTRY = 2 * BOX;
-  static constexpr int RS = 4, RV = 4;          // ring entries for S, for V
-  static constexpr int RING = RS + RV;
+  static constexpr int RING = 8;
   static constexpr int SE = 5, VE = 4;          // entries of S, of V per block
   static constexpr int THREADS = 384;
   static constexpr int SM0 = 4, SOFTMAX_WARPS = 8;
@@ -108,7 +109,7 @@ struct DenseTile {
   static constexpr int P_BYTES = HB * NK * 2;
   static constexpr int OFF_RED = OFF_P + P_BYTES;              // [2 parity][4 parts][64 heads] fp32
   static constexpr int OFF_BAR = OFF_RED + 2 * 4 * HB * 4;
-  static constexpr int NUM_BARS = 3 * RING + 10;
+  static constexpr int NUM_BARS = 4 * RING + 10;
   static constexpr int OFF_SCAN = OFF_BAR + NUM_BARS * 8;      // dense_share_block's scratch, TMEM address
   static constexpr int SMEM_BYTES = OFF_SCAN + (THREADS / 32 + 2) * 8 + 8;
   static_assert(SMEM_BYTES <= 232448, "shared memory");
@@ -259,8 +260,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + T::OFF_BAR);
   uint64_t* full = bars;                         // [RING] this CTA's part of the entry landed
   uint64_t* far_full = bars + T::RING;           // [RING] (CTA 0) the other CTA's part landed
-  uint64_t* empty = bars + 2 * T::RING;          // [RING] the MMAs have read the entry
-  uint64_t* q_full = bars + 3 * T::RING;         // this CTA's Q of a segment landed
+  uint64_t* empty = bars + 2 * T::RING;          // [RING][2] the MMAs have read the entry's even, odd use
+  uint64_t* q_full = bars + 4 * T::RING;         // this CTA's Q of a segment landed
   uint64_t* far_q = q_full + 1;                  // (CTA 0) the other CTA's Q landed
   uint64_t* q_empty = q_full + 2;                // the segment's last S has read Q
   uint64_t* s_full = q_full + 3;                 // [2] S of buffer b written
@@ -284,7 +285,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     for (int s = 0; s < T::RING; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&far_full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[2 * s], 1);
+      mbar_init(&empty[2 * s + 1], 1);
     }
     mbar_init(q_full, 1);
     mbar_init(far_q, 1);
@@ -313,18 +315,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
   const uint32_t tmem_base = *tmem_slot;
 
   // Every role walks the same segments and counts alike: g is the pair's
-  // running block number, es and ev the rings' running entries. A segment of n
-  // blocks is computed as S(0), S(1), V(0), S(2), V(1), ..., V(n - 1).
+  // running block number, e the ring's running entry. A segment of n blocks is
+  // computed as S(0), S(1), V(0), S(2), V(1), ..., V(n - 1).
   if (warp == 0 || warp == 2) {
     // ------------------------------------------------------------ loads
-    // Warp 0 loads Q and the S ring, warp 2 the V ring: issuing a copy takes one
-    // thread about 290 cycles, nine of them would bound a block. A ring has one
-    // loader, which waits for every entry of it in turn, so no barrier is ever
-    // more than a phase away from a waiting thread.
+    // Warp 0 loads Q and the S entries, warp 2 the V entries: issuing a copy
+    // takes one thread about 290 cycles, nine of them would bound a block. A
+    // loader waits for its own entries only: the other's may pass by more than
+    // one phase meanwhile. `empty` has a barrier for the even and one for the odd
+    // uses of a slot, so a wait for use u - 1 could be mistaken only for use u - 5,
+    // 24 entries and more before, while a loader's entries are at most 11 apart.
     const bool for_s = warp == 0;
-    uint32_t e = 0, segs = 0, tails = 0;         // e: entries of this warp's ring
+    uint32_t e0 = 0, segs = 0, tails = 0;        // e0: the segment's first entry
+    uint32_t mine = 0, phase = 0;                // slots this warp has filled, and their phases
     bool ok = true;
     DenseSeg w;
+    // The slot of entry e, once its last use has been read.
+    auto claim = [&](uint32_t e) -> uint32_t {
+      const uint32_t st = e % T::RING, u = e / T::RING;
+      if (u > 0) ok = mbar_wait(&empty[2 * st + ((u - 1) & 1)], ((u - 1) >> 1) & 1);
+      mine |= 1u << st;
+      phase = (phase & ~(1u << st)) | ((u & 1) << st);
+      return st;
+    };
     while (ok && walk.next(p, w)) {
       const int b = w.row / p.n_q;
       // The pool row of a block's first key: a block of 128 lies inside one
@@ -345,9 +358,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         ++segs;
         for (int i = 0; i < w.n && ok; ++i) {
           // S(i): this CTA's 64 keys, dims 128 t .. + 127 (the last entry: 64)
-          for (int t = 0; t < T::SE; ++t, ++e) {
-            const uint32_t st = e % T::RS;
-            ok = mbar_wait(&empty[st], ((e / T::RS) & 1) ^ 1);
+          const uint32_t e = e0 + (i == 0 ? 0 : T::SE + (i - 1) * (T::SE + T::VE));
+          for (int t = 0; t < T::SE; ++t) {
+            const uint32_t st = claim(e + t);
             if (!ok) break;
             if (lane == 0) {
               mbar_arrive_expect_tx(&full[st], T::ENTRY);
@@ -360,9 +373,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         for (int i = 0; i < w.n && ok; ++i) {
           // V(i): entry (key half kh, accumulator j): dims 256 j + 128 rank .. + 127
           const int valid = w.vis - (w.blk + i) * NK;
-          for (int t = 0; t < T::VE; ++t, ++e) {
-            const uint32_t st = T::RS + e % T::RV;
-            ok = mbar_wait(&empty[st], ((e / T::RV) & 1) ^ 1);
+          const uint32_t e = e0 + (i + 1 < w.n ? T::SE + i * (T::SE + T::VE) + T::SE
+                                               : w.n * (T::SE + T::VE) - T::VE);
+          for (int t = 0; t < T::VE; ++t) {
+            const uint32_t st = claim(e + t);
             if (!ok) break;
             const int kh = t >> 1, zb = 4 * (t & 1) + 2 * static_cast<int>(rank);
             const int rows = valid - 64 * kh;    // of this half that hold keys
@@ -393,19 +407,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           if (i + 1 < w.n) y = locate(w.blk + i + 1);
         }
       }
+      e0 += static_cast<uint32_t>(w.n) * (T::SE + T::VE);
       __syncwarp();
     }
     // A wait that ran out leaves copies in flight: they end before the CTA does.
     if (!ok) {
-      const uint32_t n = for_s ? T::RS : T::RV;
-      for (uint32_t d = 1; d <= n && d <= e; ++d)
-        mbar_wait(&full[(for_s ? 0 : T::RS) + (e - d) % n], ((e - d) / n) & 1);
+      for (uint32_t st = 0; st < T::RING; ++st)
+        if ((mine >> st) & 1u) mbar_wait(&full[st], (phase >> st) & 1u);
       if (for_s && segs > 0) mbar_wait(q_full, (segs - 1) & 1);
     }
   } else if (warp == 1 && rank == 1) {
     // ------------------------------------------------------------ arrivals passed on to CTA 0
     if (elect_one()) {
-      uint32_t es = 0, ev = 0, segs = 0;
+      uint32_t e = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
       while (ok && walk.next(p, w)) {
@@ -413,16 +427,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (!ok) break;
         mbar_arrive_at(far_q, 0);
         ++segs;
-        for (int i = 0; i <= w.n && ok; ++i) {   // in the order the MMAs read
-          for (int t = 0; t < T::SE && i < w.n && ok; ++t, ++es) {
-            ok = mbar_wait(&full[es % T::RS], (es / T::RS) & 1);
-            if (ok) mbar_arrive_at(&far_full[es % T::RS], 0);
-          }
-          for (int t = 0; t < T::VE && i > 0 && ok; ++t, ++ev) {
-            const uint32_t st = T::RS + ev % T::RV;
-            ok = mbar_wait(&full[st], (ev / T::RV) & 1);
-            if (ok) mbar_arrive_at(&far_full[st], 0);
-          }
+        const uint32_t last = e + static_cast<uint32_t>(w.n) * (T::SE + T::VE);
+        for (; e < last; ++e) {
+          ok = mbar_wait(&full[e % T::RING], (e / T::RING) & 1);
+          if (!ok) break;
+          mbar_arrive_at(&far_full[e % T::RING], 0);
         }
       }
     }
@@ -436,13 +445,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const uint64_t v_desc0 = umma_desc(smem_u32(ring), T::BOX, 1024, 2);
       const uint64_t q_desc0 = umma_desc(smem_u32(q_smem), 16, 1024, 2);
       const uint64_t p_desc0 = umma_desc(smem_u32(smem + T::OFF_P), 16, 1024, 2);
-      uint32_t es = 0, ev = 0, g = 0, segs = 0;
+      uint32_t e = 0, g = 0, segs = 0;
       bool ok = true;
       DenseSeg w;
-      auto landed = [&](uint32_t st, uint32_t ph) {
+      // Entry e has landed in both CTAs; its slot.
+      auto landed = [&]() -> uint32_t {
+        const uint32_t st = e % T::RING, ph = (e / T::RING) & 1;
         ok = mbar_wait(&full[st], ph) && mbar_wait(&far_full[st], ph);
         tc_fence_after();
-        return ok;
+        return st;
+      };
+      // Its MMAs have been issued: free once they finish.
+      auto release = [&]() {
+        umma_commit_pair(&empty[2 * (e % T::RING) + ((e / T::RING) & 1)]);
+        ++e;
       };
       while (ok && walk.next(p, w)) {
         ok = mbar_wait(q_full, segs & 1) && mbar_wait(far_q, segs & 1);
@@ -457,8 +473,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
             const uint32_t d = tmem_base + T::COL_S + b * 64;
 #pragma unroll
             for (int t = 0; t < T::SE; ++t) {
-              const uint32_t st = es % T::RS;
-              if (!landed(st, (es / T::RS) & 1)) break;
+              const uint32_t st = landed();
+              if (!ok) break;
               const uint64_t kd = k_desc0 + static_cast<uint32_t>(st * (T::ENTRY >> 4));
 #pragma unroll
               for (int kk = 0; kk < (t < 4 ? 8 : 4); ++kk) {
@@ -466,8 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
                 umma_bf16_ss_pair(d, q_desc0 + (t * (T::ENTRY >> 4) + off), kd + off, idesc_s,
                                   (t | kk) ? 1u : 0u);
               }
-              umma_commit_pair(&empty[st]);
-              ++es;
+              release();
             }
             if (!ok) break;
             umma_commit_pair(&s_full[b]);
@@ -481,16 +496,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const uint32_t more_o = i > 1 ? 1u : 0u;   // a segment's first product overwrites O
 #pragma unroll
           for (int t = 0; t < T::VE; ++t) {
-            const uint32_t st = T::RS + ev % T::RV;
-            if (!landed(st, (ev / T::RV) & 1)) break;
+            const uint32_t st = landed();
+            if (!ok) break;
             const uint64_t vd = v_desc0 + static_cast<uint32_t>(st * (T::ENTRY >> 4));
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               umma_bf16_ss_pair(tmem_base + T::COL_O + (t & 1) * 128,
                                 p_desc0 + (((t >> 1) * T::BOX + kk * 32) >> 4), vd + ((kk * 2048) >> 4),
                                 idesc_pv, (t > 1 || kk > 0) ? 1u : more_o);
-            umma_commit_pair(&empty[st]);
-            ++ev;
+            release();
           }
           if (ok) umma_commit_pair(pv_done);
         }
