@@ -885,8 +885,10 @@ void launch_rope_t(const dsa::RopeParams& p, unsigned grid, int smem, cudaStream
 
 // ------------------------------------------------------------------ layer norm
 
-// Threads per row by width: 8 elements a thread, 16 where that would need
-// the next size of group anyway.
+// Threads per row by width: 8 elements a thread, 16 where that would need the
+// next size of group anyway. (16 elements in half as many threads for rows of up
+// to 256: 9.0 us instead of 9.3 for 65536 bf16 rows of 128, 26.4 instead of 23.5
+// for fp32 rows of 256.)
 struct NormPick {
   int tpr, nv;
 };
@@ -1749,12 +1751,17 @@ dsa_status dsa_cache_append(const dsa_shape* s, const dsa_layout* layout, const 
   p.km = lay.km;
   p.n_q = s->n_q;
   p.n_kv = s->n_kv;
-  p.tokens = static_cast<long long>(s->batch) * s->n_q;
+  p.tokens = static_cast<uint32_t>(s->batch) * static_cast<uint32_t>(s->n_q);   // at most 2^30
   p.eps = eps;
   p.ak = rope_angles(idx_rope);
   p.ac = rope_angles(kv_rope);
+  p.by_tokens = dsa::FastDiv::make(static_cast<uint32_t>(s->n_q));
+  // both rotations by the same angles: their cos and sin are formed once
+  p.same_angles = p.ak.pairs == p.ac.pairs && p.ak.amplitude == p.ac.amplitude &&
+                  std::equal(p.ak.turns, p.ak.turns + p.ak.pairs, p.ac.turns);
+  p.key_vec = p.ak.begin % 4 == 0 && (p.ak.half ? p.ak.pairs : 2 * p.ak.pairs) % 4 == 0;
   const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps, 12ll * num_sms()));
+      std::min<int64_t>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps, 10ll * num_sms()));
   constexpr int threads = 32 * dsa::kAppendWarps;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   if (s->idx_dim == 128) {

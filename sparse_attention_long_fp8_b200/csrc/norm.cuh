@@ -211,8 +211,8 @@ template <int TPR>
 constexpr int norm_threads() { return TPR <= 32 ? 256 : TPR; }
 
 // How a group keeps bytes in flight: narrow rows are loaded U at a time, wide
-// ones one row ahead (PRE); a row of two chunks per thread leaves no registers
-// for either and relies on the other CTAs. MIN_CTAS per SM bounds the registers.
+// ones one row ahead (PRE), the others rely on the other CTAs. MIN_CTAS per SM
+// bounds the registers.
 template <int TPR, int NV, int TYPE>
 struct NormFlow {
   static constexpr int U = TPR <= 32 && NV == 1 ? (TYPE == kRowBf16 ? 4 : 2) : 1;
@@ -265,12 +265,17 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::
       const float mean = norm_sum<TPR>(s, slots, buf) * inv;
       float q = 0.f;
 #pragma unroll
-      for (int j = 0; j < EPT; ++j) {
-        x[j] -= mean;
-        if (Row::elem(lane, j) < p.dim) q = fmaf(x[j], x[j], q);
+      for (int j0 = 0; j0 < EPT; j0 += VEC ? 8 : 1) {
+        float part = 0.f;
+#pragma unroll
+        for (int j = j0; j < j0 + (VEC ? 8 : 1); ++j) {
+          x[j] -= mean;
+          part = fmaf(x[j], x[j], part);
+        }
+        if (Row::elem(lane, j0) < p.dim) q += part;      // a chunk is inside the row or outside
       }
       const float var = norm_sum<TPR>(q, slots, buf) * inv;
-      const float rstd = 1.0f / sqrtf(var + p.eps);
+      const float rstd = rsqrtf(var + p.eps);
       if (r < p.rows) {
         if constexpr (!F::KEEP) {
           norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
@@ -348,8 +353,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
       float sg = 0.f, sgx = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
-        // past the row's end d is 0 and so are its products
-        x[j] = RowX::elem(lane, j) < p.dim ? (x[j] - mean[u]) * rstd[u] : 0.f;
+        // past the row's end d is 0, and with it every product
+        x[j] = (x[j] - mean[u]) * rstd[u];
         if (there) {
           aw[j] = fmaf(d[j], x[j], aw[j]);
           ab[j] += d[j];
@@ -385,7 +390,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
         float v = k == 0 ? aw[j] : ab[j];
-        if constexpr (TPR == 16) v += __shfl_xor_sync(0xffffffffu, v, 16);
+#pragma unroll
+        for (int o = TPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
         acc[threadIdx.x >> 5][RowX::elem(lane, j)] = v;
       }
       __syncthreads();
