@@ -9,6 +9,7 @@ call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -423,6 +424,11 @@ def rope_spec(rot_dim, rot_begin=0, layout=DSA_ROPE_HALF, base=10000.0, scaling=
     return spec
 
 
+@functools.lru_cache(maxsize=256)
+def _rope_view(shape, dtype, x_stride, out_stride):
+    return DsaRopeView(*shape, dtype, x_stride[:3], out_stride[:3])
+
+
 def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=None):
     """Rotary positions: out = x [B, T, H, D] (bf16 or fp32, any strides, D
     contiguous) with the spec's dims turned by each token's position; out may
@@ -441,8 +447,7 @@ def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=Non
     rp = _arg(row_pos, _I32, (B, T), dev, "row_pos")
     if dev >= 0 and 0 in shape:
         return
-    view = DsaRopeView(B, T, H, D, code, xs[:3], os_[:3])
-    _launch(load_library().dsa_rope, dev, stream, spec, view, x.data_ptr(), out.data_ptr(), p0, rp,
+    _launch(load_library().dsa_rope, dev, stream, spec, _rope_view(shape, code, xs, os_), x.data_ptr(), out.data_ptr(), p0, rp,
             1 if backward else 0)
 
 

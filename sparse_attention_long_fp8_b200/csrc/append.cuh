@@ -8,9 +8,10 @@
 // (the others are copied).
 //
 // A warp takes one token. Floor: HBM, 2 (d^I + D_qk) bytes read and d^I + 4 + 2
-// D_qk written per token. What bounds it is issuing: about 400 instructions per
-// token and warp, of which the reductions, the encoding and one pair's cos and
-// sin are the most. A decode step is bound by its launch.
+// D_qk written per token. What bounds it is issuing, 440 instructions per token
+// and warp: 20 us for 26 K tokens, 3.5 TB/s. (Two tokens per warp, 16 lanes
+// each: 21 us, the registers spill; the next token's loads issued ahead: 21 us.)
+// A decode step is bound by its launch.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -46,7 +47,8 @@ struct AppendParams {
 // Token `tok` by one warp; key, cs: its scratch (DI values, pairs).
 template <int DI, int DQK>
 __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok, int lane, float* key,
-                                             float2* cs, const double* tk, const double* tc) {
+                                             float2* cs, const double* tk, const double* tc,
+                                             const float (&w)[DI / 32], const float (&bias)[DI / 32]) {
   constexpr int PER = DI / 32;     // key values of a lane
   const uint32_t b = p.by_tokens.div(tok);
   const int i = static_cast<int>(tok - b * static_cast<uint32_t>(p.n_q));
@@ -118,10 +120,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
   }
   const float rstd = rsqrtf(warp_sum(s) * (1.0f / DI) + p.eps);
 #pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = lane * PER + j;
-    v[j] = fmaf(v[j] * rstd, p.w ? __ldg(p.w + e) : 1.f, p.b ? __ldg(p.b + e) : 0.f);
-  }
+  for (int j = 0; j < PER; ++j) v[j] = fmaf(v[j] * rstd, w[j], bias[j]);
   if (!p.same_angles)
     for (int j = lane; j < p.ak.pairs; j += 32) cs[j] = rope_cos_sin(tk[j], pos, p.ak.amplitude);
   const int P = p.ak.pairs;
@@ -193,17 +192,24 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
 }
 
 template <int DI, int DQK>
-__global__ void __launch_bounds__(32 * kAppendWarps, 10) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(32 * kAppendWarps, 8) append_kernel(const __grid_constant__ AppendParams p) {
   __shared__ __align__(16) float skey[kAppendWarps][DI];
   __shared__ __align__(16) float2 scs[kAppendWarps][kRopeMaxPairs];
   __shared__ double tk[kRopeMaxPairs], tc[kRopeMaxPairs];    // turns per position
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   for (int j = threadIdx.x; j < p.ak.pairs; j += 32 * kAppendWarps) tk[j] = p.ak.turns[j];
   for (int j = threadIdx.x; j < p.ac.pairs; j += 32 * kAppendWarps) tc[j] = p.ac.turns[j];
+  constexpr int PER = DI / 32;
+  float w[PER], bias[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    w[j] = p.w ? p.w[lane * PER + j] : 1.f;
+    bias[j] = p.b ? p.b[lane * PER + j] : 0.f;
+  }
   __syncthreads();
   // no barrier below spans warps
   for (uint32_t tok = blockIdx.x * kAppendWarps + warp; tok < p.tokens; tok += gridDim.x * kAppendWarps) {
-    append_token<DI, DQK>(p, tok, lane, skey[warp], scs[warp], tk, tc);
+    append_token<DI, DQK>(p, tok, lane, skey[warp], scs[warp], tk, tc, w, bias);
     __syncwarp();                  // the scratch has been read
   }
 }

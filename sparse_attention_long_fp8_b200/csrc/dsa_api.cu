@@ -1761,7 +1761,7 @@ dsa_status dsa_cache_append(const dsa_shape* s, const dsa_layout* layout, const 
                   std::equal(p.ak.turns, p.ak.turns + p.ak.pairs, p.ac.turns);
   p.key_vec = p.ak.begin % 4 == 0 && (p.ak.half ? p.ak.pairs : 2 * p.ak.pairs) % 4 == 0;
   const unsigned grid = static_cast<unsigned>(
-      std::min<int64_t>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps, 10ll * num_sms()));
+      std::min<int64_t>((p.tokens + dsa::kAppendWarps - 1) / dsa::kAppendWarps, 8ll * num_sms()));
   constexpr int threads = 32 * dsa::kAppendWarps;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   if (s->idx_dim == 128) {
