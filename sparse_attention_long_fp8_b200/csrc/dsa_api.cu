@@ -904,34 +904,61 @@ NormPick norm_pick(int dim) {
 }
 int norm_groups(int tpr) { return tpr <= 32 ? 256 / tpr : 1; }
 
-// CTAs of the two kernels: they walk the rows, so as many as are resident
-// (the kernels' register bounds: MIN_CTAS), fewer when there are few rows.
-unsigned norm_grid(int64_t rows, int dim, bool gradient) {
-  const NormPick k = norm_pick(dim);
-  const int64_t need = (rows + norm_groups(k.tpr) - 1) / norm_groups(k.tpr);
+// Threads per row of the wide rows' kernels (whole aligned 16-byte chunks), 16
+// elements a thread; 0 for rows that the other kernel takes.
+int norm_wide_tpr(int dim, bool gradient) {
+  if (dim <= (gradient ? 1024 : 2048)) return 0;
+  return dim <= 2048 ? 128 : dim <= 4096 ? 256 : dim <= 8192 ? 512 : 1024;
+}
+
+// CTAs of a kernel: they walk the rows, so as many as are resident (its launch
+// bounds), fewer when there are few rows.
+unsigned norm_grid(int64_t rows, int dim, bool gradient, bool wide) {
   int per_sm;
-  if (gradient) per_sm = k.tpr <= 32 ? 2 : (k.tpr == 128 ? 4 : 1);
-  else per_sm = k.tpr <= 32 ? 4 : (k.tpr == 128 ? 6 : (k.tpr == 512 ? 2 : 1));
-  return static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(need, static_cast<int64_t>(num_sms()) * per_sm)));
+  int64_t groups = 1;
+  if (wide) {
+    per_sm = dsa::norm_wide_ctas(norm_wide_tpr(dim, gradient), gradient);
+  } else {
+    const int tpr = norm_pick(dim).tpr;
+    groups = norm_groups(tpr);
+    per_sm = gradient ? (tpr <= 32 ? 2 : (tpr == 128 ? 4 : 1)) : (tpr <= 32 ? 4 : (tpr == 128 ? 6 : (tpr == 512 ? 2 : 1)));
+  }
+  const int64_t most = static_cast<int64_t>(num_sms()) * per_sm;
+  return static_cast<unsigned>(std::max<int64_t>(1, std::min((rows + groups - 1) / groups, most)));
+}
+// Partial rows that the gradient's weight sums may need, aligned or not.
+unsigned norm_bwd_partials(int64_t rows, int dim) {
+  const unsigned n = norm_grid(rows, dim, true, false);
+  return norm_wide_tpr(dim, true) ? std::max(n, norm_grid(rows, dim, true, true)) : n;
+}
+
+// Stages of `bytes` that a wide row's kernel keeps in shared memory: what fits
+// one of per_sm CTAs.
+constexpr int kNormMaxSmem = 227 * 1024 - 4096;
+int norm_stages(int per_sm, size_t bytes) {
+  // reserved and static memory apart; the barriers
+  const size_t room = std::min(kNormMaxSmem, 227 * 1024 / per_sm - 1536) - 128;
+  return static_cast<int>(std::max<size_t>(1, std::min<size_t>(dsa::kNormMaxStages, room / bytes)));
 }
 
 // The element types are compiled in where rows are narrow (dim <= 256: more
 // rows fit the registers); elsewhere the kernel is told at run time.
 template <bool VEC, int TPR, int NV>
 void launch_norm_t(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
-  constexpr int threads = dsa::norm_threads<TPR>();
-  if constexpr (VEC && TPR <= 32 && NV == 1) {
-    if (p.x_bf16) dsa::norm_kernel<VEC, TPR, NV, dsa::kRowBf16><<<grid, threads, 0, st>>>(p);
-    else dsa::norm_kernel<VEC, TPR, NV, dsa::kRowF32><<<grid, threads, 0, st>>>(p);
+  using namespace dsa;
+  constexpr int threads = norm_threads<TPR>();
+  if constexpr (VEC && NV == 1) {
+    if (p.x_bf16) norm_kernel<VEC, TPR, NV, kRowBf16><<<grid, threads, 0, st>>>(p);
+    else norm_kernel<VEC, TPR, NV, kRowF32><<<grid, threads, 0, st>>>(p);
   } else {
-    dsa::norm_kernel<VEC, TPR, NV, dsa::kRowAny><<<grid, threads, 0, st>>>(p);
+    norm_kernel<VEC, TPR, NV, kRowAny><<<grid, threads, 0, st>>>(p);
   }
 }
 template <bool VEC, int TPR, int NV>
 void launch_norm_bwd_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
   using namespace dsa;
   constexpr int threads = norm_threads<TPR>();
-  if constexpr (VEC && TPR <= 32 && NV == 1) {
+  if constexpr (VEC && NV == 1) {
     if (p.x_bf16 && p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowBf16><<<grid, threads, 0, st>>>(p);
     else if (p.x_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowF32><<<grid, threads, 0, st>>>(p);
     else if (p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowF32, kRowBf16><<<grid, threads, 0, st>>>(p);
@@ -940,33 +967,80 @@ void launch_norm_bwd_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t 
     norm_bwd_kernel<VEC, TPR, NV, kRowAny, kRowAny><<<grid, threads, 0, st>>>(p);
   }
 }
-template <bool VEC>
-void launch_norm(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
-  const NormPick k = norm_pick(p.dim);
-  switch (k.tpr * 4 + k.nv) {
-    case 16 * 4 + 1: launch_norm_t<VEC, 16, 1>(p, grid, st); break;
-    case 32 * 4 + 1: launch_norm_t<VEC, 32, 1>(p, grid, st); break;
-    case 32 * 4 + 2: launch_norm_t<VEC, 32, 2>(p, grid, st); break;
-    case 128 * 4 + 1: launch_norm_t<VEC, 128, 1>(p, grid, st); break;
-    case 128 * 4 + 2: launch_norm_t<VEC, 128, 2>(p, grid, st); break;
-    case 512 * 4 + 1: launch_norm_t<VEC, 512, 1>(p, grid, st); break;
-    case 512 * 4 + 2: launch_norm_t<VEC, 512, 2>(p, grid, st); break;
-    default: launch_norm_t<VEC, 1024, 2>(p, grid, st); break;
-  }
+template <int TPR, int NV>
+dsa_status launch_norm_wide_t(const dsa::NormParams& p, unsigned grid, cudaStream_t st, int dev) {
+  static std::atomic<bool> attr_done[kMaxDevices];
+  if (dsa_status e = set_smem(dsa::norm_wide_kernel<TPR, NV>, kNormMaxSmem, dev, attr_done)) return e;
+  const size_t bytes = static_cast<size_t>(p.dim) * (p.x_bf16 ? 2 : 4);
+  const int stages = norm_stages(dsa::norm_wide_ctas(TPR, false), bytes);
+  dsa::norm_wide_kernel<TPR, NV><<<grid, TPR, 128 + stages * bytes, st>>>(p, stages);
+  return DSA_OK;
 }
-template <bool VEC>
-void launch_norm_bwd(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
-  const NormPick k = norm_pick(p.dim);
-  switch (k.tpr * 4 + k.nv) {
-    case 16 * 4 + 1: launch_norm_bwd_t<VEC, 16, 1>(p, grid, st); break;
-    case 32 * 4 + 1: launch_norm_bwd_t<VEC, 32, 1>(p, grid, st); break;
-    case 32 * 4 + 2: launch_norm_bwd_t<VEC, 32, 2>(p, grid, st); break;
-    case 128 * 4 + 1: launch_norm_bwd_t<VEC, 128, 1>(p, grid, st); break;
-    case 128 * 4 + 2: launch_norm_bwd_t<VEC, 128, 2>(p, grid, st); break;
-    case 512 * 4 + 1: launch_norm_bwd_t<VEC, 512, 1>(p, grid, st); break;
-    case 512 * 4 + 2: launch_norm_bwd_t<VEC, 512, 2>(p, grid, st); break;
-    default: launch_norm_bwd_t<VEC, 1024, 2>(p, grid, st); break;
+template <int TPR, int NV>
+dsa_status launch_norm_bwd_wide_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st, int dev) {
+  static std::atomic<bool> attr_done[kMaxDevices];
+  if (dsa_status e = set_smem(dsa::norm_bwd_wide_kernel<TPR, NV>, kNormMaxSmem, dev, attr_done)) return e;
+  const size_t bytes = static_cast<size_t>(p.dim) * ((p.x_bf16 ? 2 : 4) + (p.dy_bf16 ? 2 : 4));
+  const int stages = norm_stages(dsa::norm_wide_ctas(TPR, true), bytes);
+  dsa::norm_bwd_wide_kernel<TPR, NV><<<grid, TPR, 128 + stages * bytes, st>>>(p, stages);
+  return DSA_OK;
+}
+
+dsa_status launch_norm(const dsa::NormParams& p, bool vec, cudaStream_t st, int dev) {
+  const int wide = vec ? norm_wide_tpr(p.dim, false) : 0;
+  const unsigned grid = norm_grid(p.rows, p.dim, false, wide != 0);
+  switch (wide) {
+    case 256: return launch_norm_wide_t<256, 2>(p, grid, st, dev);
+    case 512: return launch_norm_wide_t<512, 2>(p, grid, st, dev);
+    case 1024: return launch_norm_wide_t<1024, 2>(p, grid, st, dev);
+    default: break;
   }
+  const NormPick k = norm_pick(p.dim);
+  switch ((k.tpr * 8 + k.nv) * 2 + vec) {
+    case (16 * 8 + 1) * 2 + 1: launch_norm_t<true, 16, 1>(p, grid, st); break;
+    case (32 * 8 + 1) * 2 + 1: launch_norm_t<true, 32, 1>(p, grid, st); break;
+    case (32 * 8 + 2) * 2 + 1: launch_norm_t<true, 32, 2>(p, grid, st); break;
+    case (128 * 8 + 1) * 2 + 1: launch_norm_t<true, 128, 1>(p, grid, st); break;
+    case (128 * 8 + 2) * 2 + 1: launch_norm_t<true, 128, 2>(p, grid, st); break;
+    case (16 * 8 + 1) * 2: launch_norm_t<false, 16, 1>(p, grid, st); break;
+    case (32 * 8 + 1) * 2: launch_norm_t<false, 32, 1>(p, grid, st); break;
+    case (32 * 8 + 2) * 2: launch_norm_t<false, 32, 2>(p, grid, st); break;
+    case (128 * 8 + 1) * 2: launch_norm_t<false, 128, 1>(p, grid, st); break;
+    case (128 * 8 + 2) * 2: launch_norm_t<false, 128, 2>(p, grid, st); break;
+    case (512 * 8 + 1) * 2: launch_norm_t<false, 512, 1>(p, grid, st); break;
+    case (512 * 8 + 2) * 2: launch_norm_t<false, 512, 2>(p, grid, st); break;
+    default: launch_norm_t<false, 1024, 2>(p, grid, st); break;
+  }
+  return DSA_OK;
+}
+// Also gives the number of partial rows it writes.
+dsa_status launch_norm_bwd(const dsa::NormBwdParams& p, bool vec, cudaStream_t st, int dev, int* partials) {
+  const int wide = vec ? norm_wide_tpr(p.dim, true) : 0;
+  const unsigned grid = norm_grid(p.rows, p.dim, true, wide != 0);
+  *partials = static_cast<int>(grid);
+  switch (wide) {
+    case 128: return launch_norm_bwd_wide_t<128, 2>(p, grid, st, dev);
+    case 256: return launch_norm_bwd_wide_t<256, 2>(p, grid, st, dev);
+    case 512: return launch_norm_bwd_wide_t<512, 2>(p, grid, st, dev);
+    case 1024: return launch_norm_bwd_wide_t<1024, 2>(p, grid, st, dev);
+    default: break;
+  }
+  const NormPick k = norm_pick(p.dim);
+  switch ((k.tpr * 8 + k.nv) * 2 + vec) {
+    case (16 * 8 + 1) * 2 + 1: launch_norm_bwd_t<true, 16, 1>(p, grid, st); break;
+    case (32 * 8 + 1) * 2 + 1: launch_norm_bwd_t<true, 32, 1>(p, grid, st); break;
+    case (32 * 8 + 2) * 2 + 1: launch_norm_bwd_t<true, 32, 2>(p, grid, st); break;
+    case (128 * 8 + 1) * 2 + 1: launch_norm_bwd_t<true, 128, 1>(p, grid, st); break;
+    case (16 * 8 + 1) * 2: launch_norm_bwd_t<false, 16, 1>(p, grid, st); break;
+    case (32 * 8 + 1) * 2: launch_norm_bwd_t<false, 32, 1>(p, grid, st); break;
+    case (32 * 8 + 2) * 2: launch_norm_bwd_t<false, 32, 2>(p, grid, st); break;
+    case (128 * 8 + 1) * 2: launch_norm_bwd_t<false, 128, 1>(p, grid, st); break;
+    case (128 * 8 + 2) * 2: launch_norm_bwd_t<false, 128, 2>(p, grid, st); break;
+    case (512 * 8 + 1) * 2: launch_norm_bwd_t<false, 512, 1>(p, grid, st); break;
+    case (512 * 8 + 2) * 2: launch_norm_bwd_t<false, 512, 2>(p, grid, st); break;
+    default: launch_norm_bwd_t<false, 1024, 2>(p, grid, st); break;
+  }
+  return DSA_OK;
 }
 
 dsa_status check_norm_shape(int64_t rows, int32_t dim) {
@@ -1627,9 +1701,8 @@ dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dty
   p.x_bf16 = x_dtype == DSA_BF16;
   p.y_bf16 = y_dtype == DSA_BF16;
   p.eps = eps;
-  const unsigned grid = norm_grid(rows, dim, false);
-  if (dim % 8 == 0 && norm_vec(tx) && norm_vec(ty) && aligned(weight, 16) && aligned(bias, 16)) launch_norm<true>(p, grid, static_cast<cudaStream_t>(stream));
-  else launch_norm<false>(p, grid, static_cast<cudaStream_t>(stream));
+  const bool vec = dim % 8 == 0 && norm_vec(tx) && norm_vec(ty) && aligned(weight, 16) && aligned(bias, 16);
+  if (dsa_status e = launch_norm(p, vec, static_cast<cudaStream_t>(stream), dev)) return e;
   DSA_CUDA_TRY(cudaGetLastError(), "layer norm launch");
   return DSA_OK;
 }
@@ -1639,7 +1712,7 @@ dsa_status dsa_layernorm_bwd_workspace(int64_t rows, int32_t dim, size_t* bytes)
   *bytes = 0;
   if (dsa_status st = check_norm_shape(rows, dim)) return st;
   if (rows > 0)
-    *bytes = static_cast<size_t>(norm_grid(rows, dim, true)) * 2 * dim * sizeof(float);
+    *bytes = static_cast<size_t>(norm_bwd_partials(rows, dim)) * 2 * dim * sizeof(float);
   return DSA_OK;
 }
 
@@ -1661,8 +1734,8 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
       !aligned(dbias, 4))
     return fail(DSA_ERR_INVALID_ARG, "dsa_layernorm_bwd: fp32 arrays must be 4-byte aligned");
   const bool sums = dweight || dbias;
-  const unsigned grid = norm_grid(rows, dim, true);
-  const size_t need = sums && rows > 0 ? static_cast<size_t>(grid) * 2 * dim * sizeof(float) : 0;
+  const size_t need =
+      sums && rows > 0 ? static_cast<size_t>(norm_bwd_partials(rows, dim)) * 2 * dim * sizeof(float) : 0;
   if (need > 0) {
     if (!ws || ws_bytes < need)
       return fail(DSA_ERR_WORKSPACE, "dsa_layernorm_bwd needs %zu workspace bytes, got %zu", need,
@@ -1674,6 +1747,7 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
   if (dsa_status st = current_device(&dev)) return st;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   float* part = static_cast<float*>(ws);
+  int n = 0;                       // partial rows
   if (rows > 0) {
     dsa::NormBwdParams p{};
     p.dy = dy;
@@ -1691,13 +1765,12 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
     p.dy_bf16 = dy_dtype == DSA_BF16;
     p.x_bf16 = x_dtype == DSA_BF16;
     p.dx_bf16 = dx_dtype == DSA_BF16;
-    if (dim % 8 == 0 && norm_vec(tdy) && norm_vec(tx) && norm_vec(tdx) && aligned(weight, 16)) launch_norm_bwd<true>(p, grid, st_);
-    else launch_norm_bwd<false>(p, grid, st_);
+    const bool vec = dim % 8 == 0 && norm_vec(tdy) && norm_vec(tx) && norm_vec(tdx) && aligned(weight, 16);
+    if (dsa_status e = launch_norm_bwd(p, vec, st_, dev, &n)) return e;
     DSA_CUDA_TRY(cudaGetLastError(), "layer norm gradient launch");
   }
   if (sums) {
     const dim3 rgrid((2 * dim + 31) / 32);
-    const int n = rows > 0 ? static_cast<int>(grid) : 0;
     if (rows > 0)
       DSA_CUDA_TRY(launch_dependent(dsa::norm_bwd_reduce_kernel, rgrid, dim3(1024), 0, st_,
                                     static_cast<const float*>(part), dweight, dbias, dim, n),

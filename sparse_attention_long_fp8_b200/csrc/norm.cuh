@@ -52,16 +52,18 @@ struct NormBwdParams {
 // Element types of a row tensor as a template argument; kAny: told at run time.
 enum { kRowF32 = 0, kRowBf16 = 1, kRowAny = 2 };
 
-// One thread's elements of a row as loaded: 8 NV of them in chunks of 8
-// (VEC, 16-byte loads) or one by one, TPR apart.
-template <bool VEC, int TPR, int NV, int TYPE>
+// One thread's elements of a row as loaded: 8 NV of them in chunks of E (VEC),
+// or one by one, TPR apart. E = 8 makes 16-byte accesses of bf16 but leaves the
+// halves of fp32 sectors to two instructions, so rows with an fp32 tensor among
+// theirs take E = 4.
+template <bool VEC, int TPR, int NV, int TYPE, int E>
 struct NormRow {
-  static constexpr int EPT = 8 * NV;
-  static constexpr int PER = VEC && TYPE == kRowBf16 ? 4 : 8;    // words per chunk
-  uint32_t w[PER * NV];            // fp32 bits, or for VEC bf16 pairs in a chunk's first 4
+  static constexpr int EPT = 8 * NV, CHUNKS = EPT / E;
+  static constexpr int PER = VEC && TYPE == kRowBf16 ? E / 2 : E;    // words per chunk
+  uint32_t w[PER * CHUNKS];        // fp32 bits, or for VEC bf16 pairs in a chunk's first half
 
   __device__ __forceinline__ static int elem(int lane, int j) {
-    return VEC ? ((j >> 3) * TPR + lane) * 8 + (j & 7) : j * TPR + lane;
+    return VEC ? ((j / E) * TPR + lane) * E + j % E : j * TPR + lane;
   }
   __device__ __forceinline__ static bool is_bf16(int flag) {
     return TYPE == kRowAny ? flag != 0 : TYPE == kRowBf16;
@@ -69,19 +71,28 @@ struct NormRow {
   __device__ __forceinline__ void load(const void* base, long long off, int flag, int lane, int dim) {
     if constexpr (VEC) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int e = elem(lane, 8 * v);
-        uint4 u = make_uint4(0, 0, 0, 0), t = u;
+      for (int c = 0; c < CHUNKS; ++c) {
+        const int e = elem(lane, c * E);
+        uint32_t* v = w + c * PER;
+#pragma unroll
+        for (int k = 0; k < PER; ++k) v[k] = 0u;
+        if (e >= dim) continue;
         if (is_bf16(flag)) {
-          if (e < dim) u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off + e);
-        } else if (e < dim) {
+          const uint16_t* s = static_cast<const uint16_t*>(base) + off + e;
+          if constexpr (E == 8) {
+            const uint4 u = *reinterpret_cast<const uint4*>(s);
+            v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+          } else {
+            const uint2 u = *reinterpret_cast<const uint2*>(s);
+            v[0] = u.x; v[1] = u.y;
+          }
+        } else if constexpr (PER == E) {
           const uint4* s = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + off + e);
-          u = s[0];
-          t = s[1];
-        }
-        w[PER * v] = u.x; w[PER * v + 1] = u.y; w[PER * v + 2] = u.z; w[PER * v + 3] = u.w;
-        if constexpr (PER == 8) {
-          w[8 * v + 4] = t.x; w[8 * v + 5] = t.y; w[8 * v + 6] = t.z; w[8 * v + 7] = t.w;
+#pragma unroll
+          for (int k = 0; k < E; k += 4) {
+            const uint4 u = s[k / 4];
+            v[k] = u.x; v[k + 1] = u.y; v[k + 2] = u.z; v[k + 3] = u.w;
+          }
         }
       }
     } else {
@@ -100,7 +111,7 @@ struct NormRow {
     if (VEC && is_bf16(flag)) {
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
-        const uint32_t u = w[(j >> 3) * PER + ((j & 7) >> 1)];
+        const uint32_t u = w[(j / E) * PER + (j % E) / 2];
         f[j] = __uint_as_float((j & 1) ? (u & 0xffff0000u) : (u << 16));
       }
     } else if constexpr (!VEC || TYPE != kRowBf16) {
@@ -111,27 +122,30 @@ struct NormRow {
 };
 
 // Stores one thread's elements of a row in the same arrangement.
-template <bool VEC, int TPR, int NV>
+template <bool VEC, int TPR, int NV, int E>
 __device__ __forceinline__ void norm_store(void* base, long long off, int bf16, int lane, int dim,
                                            const float (&f)[8 * NV]) {
-  using Row = NormRow<VEC, TPR, NV, kRowAny>;
+  using Row = NormRow<VEC, TPR, NV, kRowAny, E>;
   if constexpr (VEC) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int e = Row::elem(lane, 8 * v);
+    for (int c = 0; c < 8 * NV / E; ++c) {
+      const int e = Row::elem(lane, c * E);
       if (e >= dim) continue;
+      const float* v = f + c * E;
       if (bf16) {
-        uint32_t u[4];
+        uint32_t u[E / 2];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(f[8 * v + 2 * j], f[8 * v + 2 * j + 1]);
+        for (int j = 0; j < E / 2; ++j) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
           u[j] = *reinterpret_cast<const uint32_t*>(&h);
         }
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off + e) = make_uint4(u[0], u[1], u[2], u[3]);
+        uint16_t* d = static_cast<uint16_t*>(base) + off + e;
+        if constexpr (E == 8) *reinterpret_cast<uint4*>(d) = make_uint4(u[0], u[1], u[E / 2 - 2], u[E / 2 - 1]);
+        else *reinterpret_cast<uint2*>(d) = make_uint2(u[0], u[1]);
       } else {
         float4* d = reinterpret_cast<float4*>(static_cast<float*>(base) + off + e);
-        d[0] = make_float4(f[8 * v], f[8 * v + 1], f[8 * v + 2], f[8 * v + 3]);
-        d[1] = make_float4(f[8 * v + 4], f[8 * v + 5], f[8 * v + 6], f[8 * v + 7]);
+#pragma unroll
+        for (int k = 0; k < E; k += 4) d[k / 4] = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
       }
     }
   } else {
@@ -146,10 +160,10 @@ __device__ __forceinline__ void norm_store(void* base, long long off, int bf16, 
 }
 
 // One thread's fp32 weights in a row's arrangement: `fill` where there are none.
-template <bool VEC, int TPR, int NV>
+template <bool VEC, int TPR, int NV, int E>
 __device__ __forceinline__ void norm_weights(const float* w, float fill, int lane, int dim,
                                              float (&f)[8 * NV]) {
-  using Row = NormRow<VEC, TPR, NV, kRowAny>;
+  using Row = NormRow<VEC, TPR, NV, kRowAny, E>;
 #pragma unroll
   for (int j = 0; j < 8 * NV; j += VEC ? 4 : 1) {
     const int e = Row::elem(lane, j);
@@ -224,7 +238,8 @@ struct NormFlow {
 template <bool VEC, int TPR, int NV, int TYPE>
 __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::MIN_CTAS)
     norm_kernel(const NormParams p) {
-  using Row = NormRow<VEC, TPR, NV, TYPE>;
+  constexpr int E = TYPE == kRowBf16 ? 8 : 4;
+  using Row = NormRow<VEC, TPR, NV, TYPE, E>;
   using F = NormFlow<TPR, NV, TYPE>;
   constexpr int EPT = Row::EPT, GROUPS = norm_threads<TPR>() / TPR;
   __shared__ float2 slots[TPR > 32 ? 2 * TPR / 32 : 1];
@@ -239,8 +254,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::
   if (F::PRE && base + g < p.rows) raw[0].load(p.x, (base + g) * p.xs, p.x_bf16, lane, p.dim);
   float w[EPT], b[EPT];
   if constexpr (F::KEEP) {
-    norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
-    norm_weights<VEC, TPR, NV>(p.b, 0.f, lane, p.dim, b);
+    norm_weights<VEC, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+    norm_weights<VEC, TPR, NV, E>(p.b, 0.f, lane, p.dim, b);
   }
   const float inv = 1.0f / static_cast<float>(p.dim);
   for (long long r0 = base; r0 < p.rows; r0 += step * F::U) {
@@ -265,10 +280,10 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::
       const float mean = norm_sum<TPR>(s, slots, buf) * inv;
       float q = 0.f;
 #pragma unroll
-      for (int j0 = 0; j0 < EPT; j0 += VEC ? 8 : 1) {
+      for (int j0 = 0; j0 < EPT; j0 += VEC ? E : 1) {
         float part = 0.f;
 #pragma unroll
-        for (int j = j0; j < j0 + (VEC ? 8 : 1); ++j) {
+        for (int j = j0; j < j0 + (VEC ? E : 1); ++j) {
           x[j] -= mean;
           part = fmaf(x[j], x[j], part);
         }
@@ -278,12 +293,12 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::
       const float rstd = rsqrtf(var + p.eps);
       if (r < p.rows) {
         if constexpr (!F::KEEP) {
-          norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
-          norm_weights<VEC, TPR, NV>(p.b, 0.f, lane, p.dim, b);
+          norm_weights<VEC, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+          norm_weights<VEC, TPR, NV, E>(p.b, 0.f, lane, p.dim, b);
         }
 #pragma unroll
         for (int j = 0; j < EPT; ++j) x[j] = fmaf(x[j] * rstd, w[j], b[j]);
-        norm_store<VEC, TPR, NV>(p.y, r * p.ys, p.y_bf16, lane, p.dim, x);
+        norm_store<VEC, TPR, NV, E>(p.y, r * p.ys, p.y_bf16, lane, p.dim, x);
         if (lane == 0) {
           if (p.mean) p.mean[r] = mean;
           if (p.rstd) p.rstd[r] = rstd;
@@ -306,8 +321,9 @@ struct NormBwdFlow {
 template <bool VEC, int TPR, int NV, int XT, int GT>
 __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN_CTAS)
     norm_bwd_kernel(const NormBwdParams p) {
-  using RowX = NormRow<VEC, TPR, NV, XT>;
-  using RowG = NormRow<VEC, TPR, NV, GT>;
+  constexpr int E = XT == kRowBf16 && GT == kRowBf16 ? 8 : 4;
+  using RowX = NormRow<VEC, TPR, NV, XT, E>;
+  using RowG = NormRow<VEC, TPR, NV, GT, E>;
   using F = NormBwdFlow<TPR, NV>;
   constexpr int EPT = RowX::EPT, THREADS = norm_threads<TPR>(), GROUPS = THREADS / TPR;
   constexpr int COLS = TPR * EPT;                       // columns a group covers, >= dim
@@ -330,7 +346,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
   };
   if constexpr (F::PRE) fetch(base + g, cx[0], cy[0], mean[0], rstd[0]);
   float w[EPT], aw[EPT], ab[EPT];
-  if constexpr (F::KEEP) norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
+  if constexpr (F::KEEP) norm_weights<VEC, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
 #pragma unroll
   for (int j = 0; j < EPT; ++j) aw[j] = ab[j] = 0.f;
   const float inv = 1.0f / static_cast<float>(p.dim);
@@ -349,7 +365,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
       float x[EPT], d[EPT];
       cx[u].get(x, p.x_bf16);
       cy[u].get(d, p.dy_bf16);
-      if constexpr (!F::KEEP) norm_weights<VEC, TPR, NV>(p.w, 1.f, lane, p.dim, w);
+      if constexpr (!F::KEEP) norm_weights<VEC, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
       float sg = 0.f, sgx = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
@@ -368,7 +384,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
       if (there) {
 #pragma unroll
         for (int j = 0; j < EPT; ++j) d[j] = rstd[u] * (d[j] - mg - x[j] * mgx);
-        norm_store<VEC, TPR, NV>(p.dx, r * p.dxs, p.dx_bf16, lane, p.dim, d);
+        norm_store<VEC, TPR, NV, E>(p.dx, r * p.dxs, p.dx_bf16, lane, p.dim, d);
       }
     }
     if constexpr (F::PRE) {
@@ -411,6 +427,236 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
         part[e] = aw[j];
         part[p.dim + e] = ab[j];
       }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- wide rows
+
+// Wide rows whose every 16-byte chunk is aligned. A CTA has
+// one row at a time, with many elements per thread (the sums over threads cost
+// the same for any number of them), while the rows to come are on their way into
+// a ring of stages in shared memory (bulk copies, one stage per row). A stage is
+// loaded anew after the barrier of its row's first sum, when every thread holds
+// its part of the row in registers. Issuing a copy takes a thread about 290
+// cycles, so the gradient's two are issued by two warps.
+constexpr int kNormMaxStages = 8;
+// Threads of an SM that the registers allow, without and with the gradient.
+constexpr int kNormWideThreads = 768, kNormBwdWideThreads = 512;
+constexpr int norm_wide_ctas(int tpr, bool gradient) {
+  const int n = (gradient ? kNormBwdWideThreads : kNormWideThreads) / tpr;
+  return n > 1 ? n : 1;
+}
+
+// Sums of N values per thread over the CTA's TPR threads, one barrier (`buf`
+// alternates between two sets of slots).
+template <int TPR, int N>
+__device__ __forceinline__ void norm_sums(float (&v)[N], float* slots, int& buf) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  constexpr int W = TPR / 32;
+  float* s = slots + buf * W * N;
+  buf ^= 1;
+  if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i * W + (threadIdx.x >> 5)] = v[i];
+  }
+  __syncthreads();
+  // lane k < W of every warp takes warp k's sum
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    float t = (threadIdx.x & 31) < W ? s[i * W + (threadIdx.x & 31)] : 0.f;
+#pragma unroll
+    for (int o = (W > 1 ? W / 2 : 0); o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    v[i] = __shfl_sync(0xffffffffu, t, 0);
+  }
+}
+
+struct NormRing {
+  uint8_t* data;
+  uint64_t* full;
+  int st, stages;
+  uint32_t phase;
+  bool ok;
+
+  // Every thread; `copies` arrivals complete a stage.
+  __device__ __forceinline__ void init(uint8_t* smem, int n, int copies) {
+    full = reinterpret_cast<uint64_t*>(smem);
+    data = smem + 128;
+    st = 0;
+    stages = n;
+    phase = 0;
+    ok = true;
+    if (threadIdx.x == 0) {
+      for (int k = 0; k < kNormMaxStages; ++k) mbar_init(&full[k], copies);
+      fence_mbar_init();
+    }
+    __syncthreads();
+  }
+  // The current stage has landed. A wait that runs out is reported; the thread
+  // goes on without waiting, so that every thread meets every barrier.
+  __device__ __forceinline__ void wait() {
+    if (ok) ok = mbar_wait(&full[st], phase);
+  }
+  __device__ __forceinline__ void next() {
+    if (++st == stages) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
+};
+
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, false)) norm_wide_kernel(const NormParams p, int stages) {
+  constexpr int E = 4, EPT = 8 * NV;
+  constexpr bool KEEP = TPR < 1024;              // weights stay in registers
+  using Row = NormRow<true, TPR, NV, kRowAny, E>;
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ float slots[2 * TPR / 32];
+  int buf = 0;
+  const int lane = threadIdx.x;
+  const long long step = gridDim.x;
+  const uint32_t bytes = p.dim * (p.x_bf16 ? 2 : 4);
+  NormRing ring;
+  ring.init(norm_smem, stages, 1);
+  auto copy_in = [&](long long r, int st) {
+    if (r >= p.rows) return;
+    mbar_arrive_expect_tx(&ring.full[st], bytes);
+    bulk_load(smem_u32(ring.data + st * bytes), static_cast<const uint8_t*>(p.x) + r * p.xs * (p.x_bf16 ? 2 : 4),
+              bytes, &ring.full[st]);
+  };
+  if ((lane & 31) == 0)
+    for (int k = lane >> 5; k < stages; k += TPR / 32) copy_in(blockIdx.x + k * step, k);
+  float w[EPT], b[EPT];
+  if constexpr (KEEP) {
+    norm_weights<true, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+    norm_weights<true, TPR, NV, E>(p.b, 0.f, lane, p.dim, b);
+  }
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  for (long long r = blockIdx.x; r < p.rows; r += step) {
+    float x[EPT], s[1] = {0.f}, q[1] = {0.f};
+    ring.wait();
+    {
+      Row raw;
+      raw.load(ring.data + ring.st * bytes, 0, p.x_bf16, lane, p.dim);
+      raw.get(x, p.x_bf16);
+    }
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) s[0] += x[j];
+    norm_sums<TPR, 1>(s, slots, buf);
+    if (lane == 0) copy_in(r + stages * step, ring.st);
+    ring.next();
+    const float mean = s[0] * inv;
+#pragma unroll
+    for (int j0 = 0; j0 < EPT; j0 += E) {
+      float part = 0.f;
+#pragma unroll
+      for (int j = j0; j < j0 + E; ++j) {
+        x[j] -= mean;
+        part = fmaf(x[j], x[j], part);
+      }
+      if (Row::elem(lane, j0) < p.dim) q[0] += part;
+    }
+    norm_sums<TPR, 1>(q, slots, buf);
+    const float rstd = rsqrtf(q[0] * inv + p.eps);
+    if constexpr (!KEEP) {
+      norm_weights<true, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+      norm_weights<true, TPR, NV, E>(p.b, 0.f, lane, p.dim, b);
+    }
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) x[j] = fmaf(x[j] * rstd, w[j], b[j]);
+    norm_store<true, TPR, NV, E>(p.y, r * p.ys, p.y_bf16, lane, p.dim, x);
+    if (lane == 0) {
+      if (p.mean) p.mean[r] = mean;
+      if (p.rstd) p.rstd[r] = rstd;
+    }
+  }
+}
+
+template <int TPR, int NV>
+__global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, true))
+    norm_bwd_wide_kernel(const NormBwdParams p, int stages) {
+  constexpr int E = 4, EPT = 8 * NV;
+  // Weights stay in registers where rows are short (2048: 50 us, 54 with reloads);
+  // beside 256 or more threads' rows they cost more than their reloads (8191 fp32
+  // rows of 4096: 77 us, 70 with reloads).
+  constexpr bool KEEP = TPR == 128;
+  using Row = NormRow<true, TPR, NV, kRowAny, E>;
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  __shared__ float slots[2 * 2 * TPR / 32];
+  int buf = 0;
+  const int lane = threadIdx.x, warp = threadIdx.x >> 5;
+  const long long step = gridDim.x;
+  const uint32_t x_bytes = p.dim * (p.x_bf16 ? 2 : 4), dy_bytes = p.dim * (p.dy_bf16 ? 2 : 4);
+  NormRing ring;
+  ring.init(norm_smem, stages, 2);
+  auto copy_in = [&](long long r, int st, int dy) {
+    if (r >= p.rows) return;
+    uint8_t* dst = ring.data + st * (x_bytes + dy_bytes) + (dy ? x_bytes : 0);
+    const uint32_t bytes = dy ? dy_bytes : x_bytes;
+    const uint8_t* src = dy ? static_cast<const uint8_t*>(p.dy) + r * p.dys * (p.dy_bf16 ? 2 : 4)
+                            : static_cast<const uint8_t*>(p.x) + r * p.xs * (p.x_bf16 ? 2 : 4);
+    mbar_arrive_expect_tx(&ring.full[st], bytes);
+    bulk_load(smem_u32(dst), src, bytes, &ring.full[st]);
+  };
+  if ((lane & 31) == 0)
+    for (int k = warp; k < 2 * stages; k += TPR / 32) copy_in(blockIdx.x + (k >> 1) * step, k >> 1, k & 1);
+  float w[EPT], aw[EPT], ab[EPT];
+  if constexpr (KEEP) norm_weights<true, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) aw[j] = ab[j] = 0.f;
+  const float inv = 1.0f / static_cast<float>(p.dim);
+  float nmean = 0.f, nrstd = 0.f;                        // of the row to come
+  auto stats = [&](long long r) {
+    if (r < p.rows) {
+      nmean = __ldg(p.mean + r);
+      nrstd = __ldg(p.rstd + r);
+    }
+  };
+  stats(blockIdx.x);
+  for (long long r = blockIdx.x; r < p.rows; r += step) {
+    const float mean = nmean, rstd = nrstd;
+    stats(r + step);
+    float x[EPT], d[EPT], s[2] = {0.f, 0.f};
+    ring.wait();
+    {
+      const uint8_t* src = ring.data + ring.st * (x_bytes + dy_bytes);
+      Row raw;
+      raw.load(src, 0, p.x_bf16, lane, p.dim);
+      raw.get(x, p.x_bf16);
+      raw.load(src + x_bytes, 0, p.dy_bf16, lane, p.dim);
+      raw.get(d, p.dy_bf16);
+    }
+    if constexpr (!KEEP) norm_weights<true, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) {
+      // past the row's end d is 0, and with it every product
+      x[j] = (x[j] - mean) * rstd;
+      aw[j] = fmaf(d[j], x[j], aw[j]);
+      ab[j] += d[j];
+      d[j] *= w[j];
+      s[0] += d[j];
+      s[1] = fmaf(d[j], x[j], s[1]);
+    }
+    norm_sums<TPR, 2>(s, slots, buf);
+    if ((lane & 31) == 0 && warp < 2) copy_in(r + stages * step, ring.st, warp);
+    ring.next();
+    const float mg = s[0] * inv, mgx = s[1] * inv;
+#pragma unroll
+    for (int j = 0; j < EPT; ++j) d[j] = rstd * (d[j] - mg - x[j] * mgx);
+    norm_store<true, TPR, NV, E>(p.dx, r * p.dxs, p.dx_bf16, lane, p.dim, d);
+  }
+  griddep_launch_dependents();
+  if (!p.part) return;
+  float* part = p.part + static_cast<size_t>(blockIdx.x) * 2 * p.dim;
+#pragma unroll
+  for (int j = 0; j < EPT; ++j) {
+    const int e = Row::elem(lane, j);
+    if (e < p.dim) {
+      part[e] = aw[j];
+      part[p.dim + e] = ab[j];
     }
   }
 }
