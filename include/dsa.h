@@ -448,7 +448,8 @@ dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dty
  *   and stride). weight NULL = 1. dweight and dbias [dim] fp32 may be NULL.
  *   The row sums are fp32, in a fixed order: the same bits on every call.
  *   Workspace: dsa_layernorm_bwd_workspace bytes, 16-byte aligned (none is
- *   needed when dweight and dbias are both NULL).
+ *   needed when dweight and dbias are both NULL). Calls that may overlap on
+ *   the GPU need a workspace each.
  */
 dsa_status dsa_layernorm_bwd_workspace(int64_t rows, int32_t dim, size_t* bytes);
 dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t dy_dtype,

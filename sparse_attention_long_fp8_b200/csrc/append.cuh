@@ -53,7 +53,8 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
   const uint32_t b = p.by_tokens.div(tok);
   const int i = static_cast<int>(tok - b * static_cast<uint32_t>(p.n_q));
   if (p.n_new && i >= p.n_new[b]) return;
-  const int pos = (p.q_pos0 ? p.q_pos0[b] : 0) + i;
+  // past INT_MAX it turns negative, and is reported like any position past the cache
+  const int pos = static_cast<int>(static_cast<uint32_t>(p.q_pos0 ? p.q_pos0[b] : 0) + static_cast<uint32_t>(i));
   // loads first: the key, and the latent row's 16-byte chunks
   const __nv_bfloat16* kr = p.k + static_cast<size_t>(tok) * DI + lane * PER;
   float v[PER];

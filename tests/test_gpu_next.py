@@ -283,6 +283,24 @@ def test_layernorm_no_rows_strides_and_in_place():
     assert torch.equal(x, y)
 
 
+@pytest.mark.parametrize("rows,dim", [(700, 128), (300, 512), (250, 2048), (600, 4096), (5, 16384), (40, 1001)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_layernorm_gradient_in_place(rows, dim, dtype):
+    g = _gen(dim)
+    x, dy, w = _randn(g, rows, dim, dtype=dtype), _randn(g, rows, dim, dtype=dtype), _randn(g, dim)
+    mean, rstd, y = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty_like(x)
+    dsa.dsa_layernorm(x, w, None, 1e-6, y, mean, rstd)
+    z = x.clone()
+    dsa.dsa_layernorm(z, w, None, 1e-6, z)
+    assert torch.equal(z, y)
+    want = torch.empty_like(x)
+    dsa.dsa_layernorm_bwd(dy, x, w, mean, rstd, want)
+    a, b = dy.clone(), x.clone()
+    dsa.dsa_layernorm_bwd(a, x, w, mean, rstd, a)
+    dsa.dsa_layernorm_bwd(dy, b, w, mean, rstd, b)
+    assert torch.equal(a, want) and torch.equal(b, want)
+
+
 # ------------------------------------------------------------------ cache append
 
 def _cache(B, room, page, idx, qk, seed):
@@ -357,6 +375,13 @@ def test_append_constant_key_and_reported_positions():
     c = torch.ones(2, 2, 576, device=DEV, dtype=torch.bfloat16)
     ca = _cache(2, 128, 128, 128, 576, 1)
     rk, rc = dsa.rope_spec(64), dsa.rope_spec(64, rot_begin=512)
+    # positions past INT_MAX are reported, and nothing is written
+    dsa.dsa_cache_append(shape, k, None, None, 1e-6, rk, c, rc,
+                         torch.tensor([2147483647, -7], dtype=torch.int32, device=DEV), None, ca["codes"],
+                         ca["scale"], ca["kv"], layout=ca["layout"])
+    with pytest.raises(dsa.DsaError):
+        dsa.dsa_check()
+    assert (ca["scale"] == 3.0).all() and (ca["kv"] == 5.0).all()
     pos0 = torch.tensor([126, 127], dtype=torch.int32, device=DEV)   # the last token lies past the cache
     dsa.dsa_cache_append(shape, k, None, None, 1e-6, rk, c, rc, pos0, None, ca["codes"], ca["scale"],
                          ca["kv"], layout=ca["layout"])
@@ -442,6 +467,16 @@ def test_dense(lens, T, H, page, dtype):
     _check_dense(c, out, lse, [[n - T + 1 + i for i in range(T)] for n in lens])
     again, _ = _dense(c, dtype, lse=False)
     assert torch.equal(out, again)                                   # the same bits, without lse too
+
+
+@pytest.mark.parametrize("rows", [255, 257, 385, 1200])
+def test_dense_many_rows(rows):
+    # more rows than one warp, then than one block of threads holds at a time
+    lens = [(i * 37) % 290 for i in range(rows)]
+    c = _dense_case(lens, 1, 4, 128, rows)
+    out, lse = _dense(c)
+    dsa.dsa_check()
+    _check_dense(c, out, lse, [[n] for n in lens])
 
 
 @pytest.mark.parametrize("stale", [float("inf"), float("-inf"), 3e38])
@@ -581,6 +616,57 @@ def test_serving_step_append_then_attend():
             assert sorted(i for i in idx[b, 0].tolist() if i >= 0) == list(range(n))
         _check_dense(case, out2, lse2, seen)
         lens = now
+
+
+def test_decode_step_in_a_graph_on_another_stream():
+    """append -> rotate -> dense attention captured once and replayed as the
+    sequences grow; the same calls made one by one give the same bits."""
+    g = _gen(31)
+    B, room, H = 2, 256, 16
+    shape = dsa.DsaShape(B, 1, room, 64, 128, 512, H, 576, 512, 1.0 / 24)
+    rk, rc = dsa.rope_spec(64), dsa.rope_spec(64, rot_begin=512, layout=dsa.DSA_ROPE_INTERLEAVED)
+    ca, cb = _cache(B, room, 128, 128, 576, 31), _cache(B, room, 128, 128, 576, 31)
+    for c in (ca, cb):
+        c["kv"].fill_(math.nan)
+    pos, now = torch.zeros(B, dtype=torch.int32, device=DEV), torch.ones(B, dtype=torch.int32, device=DEV)
+    k, c1 = torch.empty(B, 1, 128, device=DEV, dtype=torch.bfloat16), torch.empty(B, 1, 576, device=DEV, dtype=torch.bfloat16)
+    q = torch.empty(B, 1, H, 576, device=DEV, dtype=torch.bfloat16)
+    ws = [dsa.alloc_workspace(shape, dsa.DSA_OP_DENSE_ATTN) for _ in range(2)]
+
+    def step(ca, q, turned, out, lse, ws):
+        dsa.dsa_cache_append(shape, k, None, None, 1e-6, rk, c1, rc, pos, None, ca["codes"], ca["scale"], ca["kv"],
+                             layout=ca["layout"])
+        dsa.dsa_rope(rc, q, turned, q_pos0=pos)
+        dsa.dsa_dense_attn(shape, turned, ca["kv"], pos, now, out, lse, *ws, layout=ca["layout"])
+
+    def bufs():
+        return torch.empty_like(q), torch.empty(B, 1, H, 512, device=DEV), torch.empty(B, 1, H, device=DEV)
+    ta, tb = bufs(), bufs()
+    for t in (k, c1, q):
+        t.copy_(_randn(g, *t.shape))
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        step(ca, q, *ta, ws[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            step(ca, q, *ta, ws[0])
+    torch.cuda.current_stream().wait_stream(st)
+    for i in range(140):
+        for t in (k, c1, q):
+            t.copy_(_randn(g, *t.shape))
+        pos.fill_(i)
+        now.fill_(i + 1)
+        st.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(st):
+            graph.replay()
+        step(cb, q, *tb, ws[1])                          # meanwhile, eagerly, on its own cache and workspace
+        torch.cuda.current_stream().wait_stream(st)
+        for x, y in zip(ta, tb):
+            assert torch.equal(x, y), i
+    dsa.dsa_check()
+    case = {"shape": shape, "q": ta[0], "kv": ca["kv"], "rows": ca["rows"]}
+    _check_dense(case, ta[1], ta[2], [[140]] * B)
 
 
 def test_training_step_of_the_indexer_key():
