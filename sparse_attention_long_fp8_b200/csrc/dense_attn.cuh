@@ -13,7 +13,8 @@
 // (32 rows of up to 1500 keys: 32.7 us without, 29.2 us with 3). A row that lies inside one
 // share is written directly; the (at most two) rows that a share's ends cut
 // leave an fp32 partial O and LSE in the workspace, and dense_combine_kernel
-// joins them in key order. The cut is derived from kv_len and the positions on
+// joins them in key order. Where no row can be longer than a few blocks, rows
+// are not cut and nothing is joined. The cut is derived from kv_len and the positions on
 // the device: the host never needs the lengths.
 //
 // The two CTAs of a pair (a cluster, two SMs) work on one block together with
@@ -57,6 +58,7 @@
 namespace dsa {
 
 constexpr int kDenseRowCost = 3;               // blocks
+constexpr int kDenseCutCost = 5;               // units
 
 struct DenseParams {
   KeyMap km;
@@ -70,6 +72,7 @@ struct DenseParams {
   int32_t rows, n_q, n_kv, H;
   int32_t out_bf16;
   int32_t pairs;               // CTA pairs of the attention kernel
+  int32_t whole;               // rows are never cut (the host's bound on their length says so)
   float scale_log2;
 
   // Keys that query row r sees, and the 128-key blocks they fill.
@@ -80,13 +83,22 @@ struct DenseParams {
     return max(0, min(last + 1, len));
   }
   __device__ __forceinline__ int blocks(int r) const { return (visible(r) + 127) >> 7; }
-  // Its length on the line.
-  __device__ __forceinline__ int units(int r) const {
-    const int nb = blocks(r);
-    return nb > 0 ? nb + kDenseRowCost : 0;
+  // Length on the line of a row that sees `vis` keys.
+  __device__ static __forceinline__ int units_of(int vis) {
+    return vis > 0 ? ((vis + 127) >> 7) + kDenseRowCost : 0;
   }
+  __device__ __forceinline__ int units(int r) const { return units_of(visible(r)); }
   __device__ __forceinline__ long long share(long long total) const {
     return max(static_cast<long long>(kDenseRowCost + 1), (total + pairs - 1) / pairs);
+  }
+  // Whether rows stay whole (the longest has `most` units). Uncut, every row has
+  // a pair to itself when there are enough, else a share runs over by half a
+  // row; cutting costs kDenseCutCost and an eighth of a unit per row for the
+  // partials and their join (64 rows of 500 to 1000 keys: 42 us cut, 32 whole;
+  // one row of 2000: 22 cut, 37 whole).
+  __device__ __forceinline__ bool keep_whole(long long share, int most) const {
+    const long long whole_cost = rows <= pairs ? most : share + most / 2;
+    return whole || whole_cost <= share + kDenseCutCost + min(rows, pairs) / 8;
   }
 };
 
@@ -124,60 +136,82 @@ struct DenseSeg {
 struct DenseWalk {
   int row;
   long long off, left;
+  bool whole;                    // rows are not cut: those that begin in the share
+  int vis;                       // keys that `row` sees, -1: to be looked up
   __device__ __forceinline__ bool next(const DenseParams& p, DenseSeg& s) {
-    if (left <= 0) return false;
-    int v = p.visible(row);
-    while (v == 0) v = p.visible(++row);     // units are left, so such a row follows
-    const int nb = (v + 127) >> 7;
-    const long long end = min(off + left, static_cast<long long>(nb + kDenseRowCost));
-    s.row = row;
-    s.blk = static_cast<int>(max(0ll, off - kDenseRowCost));
-    s.n = static_cast<int>(max(0ll, end - kDenseRowCost)) - s.blk;
-    s.vis = v;
-    s.whole = s.n == nb;
-    left -= end - off;
-    ++row;
-    off = 0;
-    return s.n > 0;                          // 0: the share ends before the row's first block
+    while (left > 0) {
+      int v = vis >= 0 ? vis : p.visible(row);
+      while (v == 0) v = p.visible(++row);   // units are left, so such a row follows
+      vis = -1;
+      const int nb = (v + 127) >> 7;
+      const long long end = min(off + left, static_cast<long long>(nb + kDenseRowCost));
+      s.row = row;
+      s.vis = v;
+      s.blk = static_cast<int>(max(0ll, off - kDenseRowCost));
+      s.n = static_cast<int>(max(0ll, end - kDenseRowCost)) - s.blk;
+      if (whole) {                           // the whole row if it begins here, else none of it
+        s.blk = 0;
+        s.n = off == 0 ? nb : 0;
+      }
+      s.whole = s.n == nb;
+      left -= end - off;
+      ++row;
+      off = 0;
+      if (s.n > 0) return true;              // 0 also where a share ends before the row's first block
+    }
+    return false;
   }
 };
 
-// The share of pair `pair`. With few rows every warp finds it by itself (32 rows
-// at a time): no barrier, one trip to memory.
-constexpr int kDenseWarpTiles = 8;
+// The share of pair `pair`. With few rows every warp finds it by itself, 32 rows
+// at a time: no barrier. This runs once per launch, with cold instruction
+// caches, so it is kept short rather than unrolled (1 to 2 us). The sums fit 32
+// bits: batch * n_kv is at most 2^30, so 256 rows have at most 2^31 + 768 units.
+constexpr int kDenseWarpRows = 256;
 __device__ __forceinline__ DenseWalk dense_share_warp(const DenseParams& p, int pair) {
   const int lane = threadIdx.x & 31;
-  int len[kDenseWarpTiles];
-#pragma unroll
-  for (int k = 0; k < kDenseWarpTiles; ++k) {
-    const int r = k * 32 + lane;
-    len[k] = r < p.rows ? p.units(r) : 0;
+  uint32_t total = 0, most = 0;
+  int vis0 = 0;                                  // of the first 32 rows
+#pragma unroll 1
+  for (int r = lane; r - lane < p.rows; r += 32) {
+    const int v = r < p.rows ? p.visible(r) : 0;
+    if (r < 32) vis0 = v;
+    const uint32_t len = DenseParams::units_of(v);
+    total += __reduce_add_sync(0xffffffffu, len);
+    most = max(most, __reduce_max_sync(0xffffffffu, len));
   }
-  long long incl[kDenseWarpTiles], total = 0;    // inclusive prefixes
-#pragma unroll
-  for (int k = 0; k < kDenseWarpTiles; ++k) {
-    incl[k] = total;
-    if (k * 32 < p.rows) {
-      long long v = len[k];
+  const uint32_t share = static_cast<uint32_t>(p.share(total));
+  const bool whole = p.keep_whole(share, static_cast<int>(most));
+  DenseWalk w{pair, 0, 0, whole, -1};
+  if (whole && p.rows <= p.pairs) {              // a pair per row
+    w.vis = pair >= p.rows ? 0 : pair < 32 ? __shfl_sync(0xffffffffu, vis0, pair & 31) : p.visible(pair);
+    w.left = DenseParams::units_of(w.vis);
+    return w;
+  }
+  const uint32_t begin = pair * share;
+  if (begin >= total) return w;
+  w.left = min(share, total - begin);
+  uint32_t base = 0;                             // units of the tiles before
+#pragma unroll 1
+  for (int r = lane; r - lane < p.rows; r += 32) {
+    const int v = r < 32 ? vis0 : (r < p.rows ? p.visible(r) : 0);
+    const uint32_t len = DenseParams::units_of(v);
+    const uint32_t sum = __reduce_add_sync(0xffffffffu, len);
+    if (begin < base + sum) {
+      uint32_t incl = len;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += u;
+        const uint32_t u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
       }
-      incl[k] += v;
-      total += __shfl_sync(0xffffffffu, v, 31);
+      const uint32_t at = base + incl - len;
+      const int src = __ffs(__ballot_sync(0xffffffffu, at <= begin && begin < at + len)) - 1;
+      w.row = r - lane + src;
+      w.off = __shfl_sync(0xffffffffu, begin - at, src);
+      w.vis = __shfl_sync(0xffffffffu, v, src);
+      break;
     }
-  }
-  const long long share = p.share(total), begin = pair * share;
-  DenseWalk w{0, 0, max(0ll, min(total, begin + share) - begin)};
-#pragma unroll
-  for (int k = 0; k < kDenseWarpTiles; ++k) {
-    const bool mine = incl[k] - len[k] <= begin && begin < incl[k];
-    const uint32_t hit = __ballot_sync(0xffffffffu, mine);
-    if (hit) {
-      w.row = k * 32 + __ffs(hit) - 1;
-      w.off = __shfl_sync(0xffffffffu, begin - (incl[k] - len[k]), __ffs(hit) - 1);
-    }
+    base += sum;
   }
   return w;
 }
@@ -188,16 +222,27 @@ __device__ __forceinline__ DenseWalk dense_share_block(const DenseParams& p, int
   constexpr int THREADS = 32 * WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   long long total = 0;
-  for (int r = threadIdx.x; r < p.rows; r += THREADS) total += p.units(r);
+  int most = 0;
+  for (int r = threadIdx.x; r < p.rows; r += THREADS) {
+    const int len = p.units(r);
+    total += len;
+    most = max(most, len);
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if (lane == 0) scan[warp] = total;
+  most = __reduce_max_sync(0xffffffffu, most);
+  // a row has at most 2^23 + 3 units, all of them fewer than 2^39
+  if (lane == 0) scan[warp] = (total << 24) | most;
   __syncthreads();
   total = 0;
 #pragma unroll
-  for (int i = 0; i < WARPS; ++i) total += scan[i];
+  for (int i = 0; i < WARPS; ++i) {
+    total += scan[i] >> 24;
+    most = max(most, static_cast<int>(scan[i] & 0xffffff));
+  }
   const long long share = p.share(total), begin = pair * share;
-  DenseWalk w{0, 0, max(0ll, min(total, begin + share) - begin)};
+  // more rows than pairs here (see the caller)
+  DenseWalk w{0, 0, max(0ll, min(total, begin + share) - begin), p.keep_whole(share, most), -1};
   for (long long base = 0, r0 = 0; r0 < p.rows && w.left > 0; r0 += THREADS) {
     // exclusive prefix of this thread's row within the tile of rows
     const int r = static_cast<int>(r0) + threadIdx.x;
@@ -307,7 +352,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     tmem_alloc_pair(tmem_slot, T::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  DenseWalk walk = p.rows <= 32 * kDenseWarpTiles ? dense_share_warp(p, pair)
+  DenseWalk walk = p.rows <= kDenseWarpRows ? dense_share_warp(p, pair)
                                                  : dense_share_block<T::THREADS / 32>(p, pair, scan);
   tc_fence_before();
   cluster_sync();                                // also: both CTAs' barriers are initialised
@@ -516,7 +561,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     // ------------------------------------------------------------ the cut; rows that see no key
     DenseSeg w;
     const bool any = walk.next(p, w);
-    if (lane == 0 && rank == 0) p.cut[pair] = any ? make_int2(w.row, w.blk) : make_int2(-1, 0);
+    if (lane == 0 && rank == 0 && !p.whole) p.cut[pair] = any ? make_int2(w.row, w.blk) : make_int2(-1, 0);
     for (int r = pair; r < p.rows; r += p.pairs)
       if (p.blocks(r) == 0) dense_empty_row(p, r, static_cast<int>(rank), lane);
   } else if (warp >= T::SM0) {

@@ -788,6 +788,11 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   p.H = s->heads;
   p.out_bf16 = out_bf16;
   p.pairs = pl.pairs;
+  // No row can be long enough to be cut: the kernel's own rule (keep_whole), with
+  // a share's least size and the longest row that the caches can hold.
+  const int most = (s->n_kv + 127) / 128 + dsa::kDenseRowCost;
+  const int cut = dsa::kDenseCutCost + std::min(p.rows, p.pairs) / 8;
+  p.whole = p.rows <= p.pairs ? most <= dsa::kDenseRowCost + 1 + cut : most / 2 <= cut;
   p.scale_log2 = s->softmax_scale * 1.4426950408889634f;
   CUtensorMap tkv, tq;
   const cuuint64_t kv_dims[3] = {64, static_cast<cuuint64_t>(lay.km.pool_rows), 9}, kv_strides[2] = {1152, 128};
@@ -799,6 +804,7 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
     return st;
   dsa::dense_attn_kernel<<<2 * pl.pairs, T::THREADS, T::SMEM_BYTES, stream>>>(tkv, tq, p);
   DSA_CUDA_TRY(cudaGetLastError(), "dense attention launch");
+  if (p.whole) return DSA_OK;
   // the fewer rows, the more partials a row may have; at most pairs - 1 rows are cut
   const bool few = p.rows <= 8;
   const dim3 jgrid(std::max(1, std::min(p.rows, p.pairs - 1)), few ? p.H : (p.H + 7) / 8);
