@@ -352,10 +352,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     tmem_alloc_pair(tmem_slot, T::TMEM_COLS);
     tmem_relinquish_pair();
   }
-  DenseWalk walk = p.rows <= kDenseWarpRows ? dense_share_warp(p, pair)
-                                                 : dense_share_block<T::THREADS / 32>(p, pair, scan);
   tc_fence_before();
-  cluster_sync();                                // also: both CTAs' barriers are initialised
+  __syncwarp();
+  cluster_arrive();                              // barriers initialised, TMEM allocated; the wait is below
+  DenseWalk walk = p.rows <= kDenseWarpRows ? dense_share_warp(p, pair)
+                                            : dense_share_block<T::THREADS / 32>(p, pair, scan);
+  __syncwarp();
+  cluster_wait();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
 
@@ -697,11 +700,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       const int slot = 2 * pair + (done.blk > 0 ? 0 : 1);
       const bool bf16_out = direct && p.out_bf16;
       const size_t out_row = static_cast<size_t>(direct ? done.row : slot) * p.H;
+      uint8_t* const out_base = static_cast<uint8_t*>(direct ? p.out : static_cast<void*>(p.part_o));
+      const int esz = bf16_out ? 2 : 4;
 #pragma unroll 1
       for (int rb = 0; rb < 2; ++rb) {
         // this thread's two heads of the 16 lanes
         float inv[2];
-        size_t at[2];
+        uint8_t* at[2];
         bool there[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -712,30 +717,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           inv[k] = pv_ok && lm != 0.f ? 1.0f / lm : 0.f;                 // NaN goes through
           const int hd = static_cast<int>(rank) * T::HB + hh;
           there[k] = hd < p.H;
-          at[k] = (out_row + hd) * T::DV + half * 256 + side * 128 + (lane & 3) * 2;
+          at[k] = out_base + ((out_row + hd) * T::DV + half * 256 + side * 128 + (lane & 3) * 2) * esz;
         }
 #pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t o[16];
-          tmem_ld_16x256b_x4(tmem_base + lane_addr + (static_cast<uint32_t>(rb * 16) << 16) + T::COL_O +
+        for (int c = 0; c < 128; c += 64) {
+          uint32_t o[32];
+          tmem_ld_16x256b_x8(tmem_base + lane_addr + (static_cast<uint32_t>(rb * 16) << 16) + T::COL_O +
                                  half * 128 + c, o);
           tmem_wait_ld();
 #pragma unroll
-          for (int b = 0; b < 4; ++b)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              if (!there[k]) continue;
-              const float x = inv[k] == 0.f ? 0.f : __uint_as_float(o[4 * b + 2 * k]) * inv[k];
-              const float y = inv[k] == 0.f ? 0.f : __uint_as_float(o[4 * b + 2 * k + 1]) * inv[k];
-              const size_t e = at[k] + c + 8 * b;
+          for (int k = 0; k < 2; ++k) {
+            if (there[k]) {
               if (bf16_out) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                *reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(p.out) + e) = v;
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                  *reinterpret_cast<__nv_bfloat162*>(at[k] + b * 16) =
+                      __floats2bfloat162_rn(__uint_as_float(o[4 * b + 2 * k]) * inv[k],
+                                            __uint_as_float(o[4 * b + 2 * k + 1]) * inv[k]);
               } else {
-                float* dst = direct ? static_cast<float*>(p.out) : p.part_o;
-                *reinterpret_cast<float2*>(dst + e) = make_float2(x, y);
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                  *reinterpret_cast<float2*>(at[k] + b * 32) =
+                      make_float2(__uint_as_float(o[4 * b + 2 * k]) * inv[k],
+                                  __uint_as_float(o[4 * b + 2 * k + 1]) * inv[k]);
               }
             }
+            at[k] += 64 * esz;
+          }
         }
       }
       if (part == 0 && head < p.H) {
@@ -768,7 +776,8 @@ constexpr int kDenseMaxPairs = 128;
 // share that does not hold its end. A head's 512 value dims go to 512 / (32 VW)
 // warps with VW dims per lane. Few rows may have a partial from every pair (one
 // long sequence: 74 of them), so they get eight warps a head (VW = 2), many
-// rows one (VW = 16). No shared memory: the attention kernel leaves none for a
+// rows two (VW = 8). Like the share search it runs once with cold instruction
+// caches: its loop over partials is not unrolled (3 us). No shared memory: the attention kernel leaves none for a
 // CTA that waits beside it.
 template <int VW>
 __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseParams p) {
@@ -836,33 +845,35 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseParams p)
   float acc[VW];
 #pragma unroll
   for (int j = 0; j < VW; ++j) acc[j] = 0.f;
-  constexpr int UN = VW <= 2 ? 16 : 2;           // partials loaded before the first is added
+  constexpr int UN = VW <= 2 ? 16 : 4;           // partials loaded before the first is added
+#pragma unroll 1
+  for (int i0 = 0; i0 < np; i0 += UN) {
+    float wk = w[0];                             // of the 32 partials that i0 is among
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const int n = min(32, np - k * 32);
-    for (int i0 = 0; i0 < n; i0 += UN) {
-      float v[UN][VW];
+    for (int k = 1; k < K; ++k) wk = (i0 >> 5) == k ? w[k] : wk;
+    float v[UN][VW];
+    const float* src = p.part_o + (static_cast<size_t>(2 * (found + i0)) * p.H + h) * 512 + dim0 + lane * V;
 #pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const bool on = i0 + u < n;
-        const float* src = p.part_o + slot(k * 32 + i0 + u) * 512 + dim0 + lane * V;
+    for (int u = 0; u < UN; ++u) {
+      const bool on = i0 + u < np;
+      const float* s_u = src + (i0 + u == 0 ? static_cast<size_t>(p.H) * 512 : 0);
 #pragma unroll
-        for (int j = 0; j < VW; j += V) {
-          if constexpr (V == 4) {
-            const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(src + j * 32)) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[u][j] = t.x; v[u][j + 1] = t.y; v[u][j + 2] = t.z; v[u][j + 3] = t.w;
-          } else {
-            const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(src + j * 32)) : make_float2(0.f, 0.f);
-            v[u][j] = t.x; v[u][j + 1] = t.y;
-          }
+      for (int j = 0; j < VW; j += V) {
+        if constexpr (V == 4) {
+          const float4 t = on ? __ldcg(reinterpret_cast<const float4*>(s_u + j * 32)) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[u][j] = t.x; v[u][j + 1] = t.y; v[u][j + 2] = t.z; v[u][j + 3] = t.w;
+        } else {
+          const float2 t = on ? __ldcg(reinterpret_cast<const float2*>(s_u + j * 32)) : make_float2(0.f, 0.f);
+          v[u][j] = t.x; v[u][j + 1] = t.y;
         }
       }
+      src += static_cast<size_t>(2 * p.H) * 512;
+    }
 #pragma unroll
-      for (int u = 0; u < UN; ++u) {
-        const float wgt = __shfl_sync(0xffffffffu, w[k], (i0 + u) & 31);
+    for (int u = 0; u < UN; ++u) {
+      const float wgt = __shfl_sync(0xffffffffu, wk, (i0 + u) & 31);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) acc[j] = fmaf(wgt, v[u][j], acc[j]);
-      }
+      for (int j = 0; j < VW; ++j) acc[j] = fmaf(wgt, v[u][j], acc[j]);
     }
   }
   const float inv = sum != 0.f ? 1.0f / sum : 0.f;     // NaN goes through

@@ -807,9 +807,9 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   if (p.whole) return DSA_OK;
   // the fewer rows, the more partials a row may have; at most pairs - 1 rows are cut
   const bool few = p.rows <= 8;
-  const dim3 jgrid(std::max(1, std::min(p.rows, p.pairs - 1)), few ? p.H : (p.H + 7) / 8);
+  const dim3 jgrid(std::max(1, std::min(p.rows, p.pairs - 1)), few ? p.H : (p.H + 3) / 4);
   DSA_CUDA_TRY(few ? launch_dependent(dsa::dense_combine_kernel<2>, jgrid, dim3(256), 0, stream, p)
-                   : launch_dependent(dsa::dense_combine_kernel<16>, jgrid, dim3(256), 0, stream, p),
+                   : launch_dependent(dsa::dense_combine_kernel<8>, jgrid, dim3(256), 0, stream, p),
                "dense attention join launch");
   return DSA_OK;
 }
