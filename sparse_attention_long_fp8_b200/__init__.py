@@ -403,6 +403,16 @@ def _arg(t, dtypes, shape, idx, what):
     return t.data_ptr()
 
 
+def _vec(t, dtype, n, idx, what):
+    """_arg for a vector of n elements of one dtype, in any shape."""
+    if t is None:
+        return None
+    if (t.dtype is not dtype or t.numel() != n or t.get_device() != idx
+            or not t.is_contiguous()):
+        return _arg(t, (dtype,), (n,), idx, what)      # says what is wrong
+    return t.data_ptr()
+
+
 def _dtype_code(t, what):
     dt = t.dtype
     if dt is torch.bfloat16:
@@ -443,7 +453,7 @@ def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=Non
     if D > 1 and (xs[3] != 1 or os_[3] != 1):
         raise ValueError("the last dim of x and out must be contiguous")
     code = _dtype_code(x, "x")
-    p0 = _arg(q_pos0, _I32, (B,), dev, "q_pos0")
+    p0 = _vec(q_pos0, torch.int32, B, dev, "q_pos0")
     rp = _arg(row_pos, _I32, (B, T), dev, "row_pos")
     if dev >= 0 and 0 in shape:
         return
@@ -465,13 +475,6 @@ def _rows(t, what):
     return (t.numel() // dim if dim else 0), dim, dim
 
 
-def _row_stat(t, rows, idx, what):
-    """Pointer of an fp32 tensor with one element per row, in any shape."""
-    if t is not None and t.numel() != rows:
-        raise ValueError(f"{what} has {t.numel()} elements, expected {rows}")
-    return _arg(t, _F32, None, idx, what)
-
-
 def dsa_layernorm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
     """Layer norm over the last dim of x into y (bf16 or fp32 each); weight and
     bias fp32 [dim] or None; mean and rstd fp32 [rows] receive the statistics."""
@@ -479,10 +482,10 @@ def dsa_layernorm(x, weight, bias, eps, y, mean=None, rstd=None, stream=None):
     dev = x.get_device()
     if x.shape != y.shape or y.get_device() != dev:
         raise ValueError("y must have x's shape and device")
-    ys = _rows(y, "y")[2]
+    ys = xs if y.stride() == x.stride() else _rows(y, "y")[2]
     xc, yc = _dtype_code(x, "x"), _dtype_code(y, "y")
-    w, b = _arg(weight, _F32, (dim,), dev, "weight"), _arg(bias, _F32, (dim,), dev, "bias")
-    m, r = _row_stat(mean, rows, dev, "mean"), _row_stat(rstd, rows, dev, "rstd")
+    w, b = _vec(weight, torch.float32, dim, dev, "weight"), _vec(bias, torch.float32, dim, dev, "bias")
+    m, r = _vec(mean, torch.float32, rows, dev, "mean"), _vec(rstd, torch.float32, rows, dev, "rstd")
     if rows == 0 and dev >= 0:
         return
     _launch(load_library().dsa_layernorm, dev, stream, rows, dim, x.data_ptr(), xc, xs, w, b, eps,
@@ -503,11 +506,13 @@ def dsa_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, w
     shape, dev = x.shape, x.get_device()
     if dy.shape != shape or dx.shape != shape or dy.get_device() != dev or dx.get_device() != dev:
         raise ValueError("dy and dx must have x's shape and device")
-    dys, dxs = _rows(dy, "dy")[2], _rows(dx, "dx")[2]
+    st = x.stride()
+    dys = xs if dy.stride() == st else _rows(dy, "dy")[2]
+    dxs = xs if dx.stride() == st else _rows(dx, "dx")[2]
     dyc, xc, dxc = _dtype_code(dy, "dy"), _dtype_code(x, "x"), _dtype_code(dx, "dx")
-    w = _arg(weight, _F32, (dim,), dev, "weight")
-    m, r = _row_stat(mean, rows, dev, "mean"), _row_stat(rstd, rows, dev, "rstd")
-    dw, db = _arg(dweight, _F32, (dim,), dev, "dweight"), _arg(dbias, _F32, (dim,), dev, "dbias")
+    w = _vec(weight, torch.float32, dim, dev, "weight")
+    m, r = _vec(mean, torch.float32, rows, dev, "mean"), _vec(rstd, torch.float32, rows, dev, "rstd")
+    dw, db = _vec(dweight, torch.float32, dim, dev, "dweight"), _vec(dbias, torch.float32, dim, dev, "dbias")
     wp = _arg(ws, (torch.uint8,), None, dev, "ws")
     ptrs = [dy.data_ptr(), x.data_ptr(), dx.data_ptr(), m, r]
     if rows == 0:      # empty tensors have no address, and nothing is read through one
@@ -533,10 +538,10 @@ def dsa_cache_append(shape, k, ln_weight, ln_bias, eps, idx_rope, c, kv_rope, q_
     if k_fp8.numel() != pool * di or k_scale.numel() != pool or kv.numel() != pool * dq:
         raise ValueError(f"k_fp8, k_scale and kv must have {pool} rows of {di}, 1 and {dq} elements")
     _launch(load_library().dsa_cache_append, dev, stream, shape, layout,
-            _arg(k, _BF16, (B, T, di), dev, "k"), _arg(ln_weight, _F32, (di,), dev, "ln_weight"),
-            _arg(ln_bias, _F32, (di,), dev, "ln_bias"), eps, idx_rope,
-            _arg(c, _BF16, (B, T, dq), dev, "c"), kv_rope, _arg(q_pos0, _I32, (B,), dev, "q_pos0"),
-            _arg(n_new, _I32, (B,), dev, "n_new"), _arg(k_fp8, _CODES, None, dev, "k_fp8"),
+            _arg(k, _BF16, (B, T, di), dev, "k"), _vec(ln_weight, torch.float32, di, dev, "ln_weight"),
+            _vec(ln_bias, torch.float32, di, dev, "ln_bias"), eps, idx_rope,
+            _arg(c, _BF16, (B, T, dq), dev, "c"), kv_rope, _vec(q_pos0, torch.int32, B, dev, "q_pos0"),
+            _vec(n_new, torch.int32, B, dev, "n_new"), _arg(k_fp8, _CODES, None, dev, "k_fp8"),
             _arg(k_scale, _F32, None, dev, "k_scale"), _arg(kv, _BITS16, None, dev, "kv"))
 
 
@@ -550,7 +555,7 @@ def dsa_dense_attn(shape, q, kv, q_pos0, kv_len, out, lse=None, ws=None, ws_byte
         raise ValueError(f"kv has {kv.numel()} elements, the cache has {pool} rows of {dq}")
     _launch(load_library().dsa_dense_attn_ex, dev, stream, shape, layout,
             _arg(q, _BITS16, (B, T, H, dq), dev, "q"), _arg(kv, _BITS16, None, dev, "kv"),
-            _arg(q_pos0, _I32, (B,), dev, "q_pos0"), _arg(kv_len, _I32, (B,), dev, "kv_len"),
+            _vec(q_pos0, torch.int32, B, dev, "q_pos0"), _vec(kv_len, torch.int32, B, dev, "kv_len"),
             _arg(out, _FLOATS, (B, T, H, shape.v_dim), dev, "out"),
             DSA_OUT_BF16 if out.dtype == torch.bfloat16 else DSA_OUT_F32,
             _arg(lse, _F32, (B, T, H), dev, "lse"), _arg(ws, (torch.uint8,), None, dev, "ws"), ws_bytes)
