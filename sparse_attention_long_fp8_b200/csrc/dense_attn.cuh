@@ -10,12 +10,12 @@
 // and one long sequence spreads over the whole GPU. A row counts kDenseRowCost
 // units more than its blocks, at its beginning: taking up a row (its Q, the
 // first block's latency, its output) costs about as much as that many blocks
-// (32 rows of up to 1500 keys: 32.7 us without, 29.2 us with 3). A row that lies inside one
-// share is written directly; the (at most two) rows that a share's ends cut
-// leave an fp32 partial O and LSE in the workspace, and dense_combine_kernel
-// joins them in key order. Where no row can be longer than a few blocks, rows
-// are not cut and nothing is joined. The cut is derived from kv_len and the positions on
-// the device: the host never needs the lengths.
+// (32 rows of up to 1500 keys: 29.7 us without, 27.2 us with 3). A row that lies
+// inside one share is written directly; the (at most two) rows that a share's
+// ends cut leave an fp32 partial O and LSE in the workspace, and
+// dense_combine_kernel joins them in key order. Where no row is longer than a few
+// blocks, rows are not cut and nothing is joined. The cut is derived from kv_len
+// and the positions on the device: the host never needs the lengths.
 //
 // The two CTAs of a pair (a cluster, two SMs) work on one block together with
 // tcgen05 over both (cta_group::2, M = 128 heads, 64 per CTA):
@@ -59,6 +59,7 @@ namespace dsa {
 
 constexpr int kDenseRowCost = 3;               // blocks
 constexpr int kDenseCutCost = 5;               // units
+constexpr int kDenseMinShare = 1;              // units (one row of 4000 keys: 14.8 us, 18.4 with 4)
 
 struct DenseParams {
   KeyMap km;
@@ -89,13 +90,13 @@ struct DenseParams {
   }
   __device__ __forceinline__ int units(int r) const { return units_of(visible(r)); }
   __device__ __forceinline__ long long share(long long total) const {
-    return max(static_cast<long long>(kDenseRowCost + 1), (total + pairs - 1) / pairs);
+    return max(static_cast<long long>(kDenseMinShare), (total + pairs - 1) / pairs);
   }
   // Whether rows stay whole (the longest has `most` units). Uncut, every row has
   // a pair to itself when there are enough, else a share runs over by half a
   // row; cutting costs kDenseCutCost and an eighth of a unit per row for the
-  // partials and their join (64 rows of 500 to 1000 keys: 42 us cut, 32 whole;
-  // one row of 2000: 22 cut, 37 whole).
+  // partials and their join (64 rows of 500 to 1000 keys: 39.5 us cut, 29.3
+  // whole; one row of 2000: 14.0 cut, 33 whole).
   __device__ __forceinline__ bool keep_whole(long long share, int most) const {
     const long long whole_cost = rows <= pairs ? most : share + most / 2;
     return whole || whole_cost <= share + kDenseCutCost + min(rows, pairs) / 8;
@@ -777,8 +778,8 @@ constexpr int kDenseMaxPairs = 128;
 // warps with VW dims per lane. Few rows may have a partial from every pair (one
 // long sequence: 74 of them), so they get eight warps a head (VW = 2), many
 // rows two (VW = 8). Like the share search it runs once with cold instruction
-// caches: its loop over partials is not unrolled (3 us). No shared memory: the attention kernel leaves none for a
-// CTA that waits beside it.
+// caches: its loop over partials is not unrolled (3 us). No shared memory: the
+// attention kernel leaves none for a CTA that waits beside it.
 template <int VW>
 __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseParams p) {
   constexpr int WPH = 512 / (32 * VW);           // warps per head

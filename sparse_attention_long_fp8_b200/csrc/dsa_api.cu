@@ -788,11 +788,14 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   p.H = s->heads;
   p.out_bf16 = out_bf16;
   p.pairs = pl.pairs;
-  // No row can be long enough to be cut: the kernel's own rule (keep_whole), with
-  // a share's least size and the longest row that the caches can hold.
+  // Rows that the kernel's own rule (keep_whole) would leave whole whatever the
+  // lengths, from a share's least size and the longest row that the caches can
+  // hold: no join is launched. With some rows the launch that this saves, 2 us,
+  // is worth a few blocks more (16 rows of 350 to 700 keys: 18.6 us, 20.5 with a
+  // join that finds nothing).
   const int most = (s->n_kv + 127) / 128 + dsa::kDenseRowCost;
-  const int cut = dsa::kDenseCutCost + std::min(p.rows, p.pairs) / 8;
-  p.whole = p.rows <= p.pairs ? most <= dsa::kDenseRowCost + 1 + cut : most / 2 <= cut;
+  p.whole = p.rows <= p.pairs ? most <= dsa::kDenseMinShare + dsa::kDenseCutCost + p.rows / 5
+                              : most / 2 <= dsa::kDenseCutCost + p.pairs / 8;
   p.scale_log2 = s->softmax_scale * 1.4426950408889634f;
   CUtensorMap tkv, tq;
   const cuuint64_t kv_dims[3] = {64, static_cast<cuuint64_t>(lay.km.pool_rows), 9}, kv_strides[2] = {1152, 128};
