@@ -9,8 +9,11 @@
 //
 // A warp takes one token. Floor: HBM, 2 (d^I + D_qk) bytes read and d^I + 4 + 2
 // D_qk written per token. What bounds it is issuing, 440 instructions per token
-// and warp: 20 us for 26 K tokens, 3.5 TB/s. (Two tokens per warp, 16 lanes
-// each: 21 us, the registers spill; the next token's loads issued ahead: 21 us.)
+// and warp, in a chain of two loads, reductions and stores that 32 warps per SM
+// hide in part: 19.7 us for 26 K tokens, 3.55 TB/s (without the key's part or
+// without the latent row's it would be 14.9). Two tokens per warp, 16 lanes each:
+// 21 us, the registers spill; the next token's loads issued ahead: 21 us; 40 or 48
+// warps per SM: 23 us, spills; loads behind the test of n_new: 20.1 us.
 // A decode step is bound by its launch.
 #pragma once
 
@@ -52,10 +55,10 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
   constexpr int PER = DI / 32;     // key values of a lane
   const uint32_t b = p.by_tokens.div(tok);
   const int i = static_cast<int>(tok - b * static_cast<uint32_t>(p.n_q));
-  if (p.n_new && i >= p.n_new[b]) return;
+  const int n_new = p.n_new ? p.n_new[b] : p.n_q;
   // past INT_MAX it turns negative, and is reported like any position past the cache
   const int pos = static_cast<int>(static_cast<uint32_t>(p.q_pos0 ? p.q_pos0[b] : 0) + static_cast<uint32_t>(i));
-  // loads first: the key, and the latent row's 16-byte chunks
+  // loads first, of a padded token's rows too: the key, and the latent row's 16-byte chunks
   const __nv_bfloat16* kr = p.k + static_cast<size_t>(tok) * DI + lane * PER;
   float v[PER];
   if constexpr (PER == 4) {
@@ -73,6 +76,7 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
 #pragma unroll
   for (int r = 0; r < ROUNDS; ++r)
     if (r * 32 + lane < CHUNKS) row[r] = reinterpret_cast<const uint4*>(cr)[r * 32 + lane];
+  if (i >= n_new) return;
   if (pos < 0 || pos >= p.n_kv) {  // past the cache: reported, nothing written
     if (lane == 0) raise_error(kErrBadInput);
     return;
