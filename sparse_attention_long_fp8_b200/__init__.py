@@ -364,7 +364,7 @@ def indexer_kl(inp: dict, cfg: DsaConfig, stream=None):
 # so the checks below read each tensor property once and build nothing.
 _F32, _I32, _BF16 = (torch.float32,), (torch.int32,), (torch.bfloat16,)
 _BITS16, _CODES = (torch.bfloat16, torch.int16), (torch.uint8, torch.float8_e4m3fn)
-_FLOATS = (torch.float32, torch.bfloat16)
+_FLOATS, _U8 = (torch.float32, torch.bfloat16), (torch.uint8,)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
@@ -413,6 +413,13 @@ def _vec(t, dtype, n, idx, what):
     return t.data_ptr()
 
 
+def _ws(ws, ws_bytes, idx):
+    """_arg for a workspace that holds the ws_bytes it is said to."""
+    if ws is not None and ws_bytes > ws.numel():
+        raise ValueError(f"ws has {ws.numel()} bytes, ws_bytes is {ws_bytes}")
+    return _arg(ws, _U8, None, idx, "ws")
+
+
 def _dtype_code(t, what):
     dt = t.dtype
     if dt is torch.bfloat16:
@@ -457,8 +464,8 @@ def dsa_rope(spec, x, out, q_pos0=None, row_pos=None, backward=False, stream=Non
     rp = _arg(row_pos, _I32, (B, T), dev, "row_pos")
     if dev >= 0 and 0 in shape:
         return
-    _launch(load_library().dsa_rope, dev, stream, spec, _rope_view(shape, code, xs, os_), x.data_ptr(), out.data_ptr(), p0, rp,
-            1 if backward else 0)
+    _launch(load_library().dsa_rope, dev, stream, spec, _rope_view(shape, code, xs, os_),
+            x.data_ptr(), out.data_ptr(), p0, rp, 1 if backward else 0)
 
 
 def _rows(t, what):
@@ -513,7 +520,7 @@ def dsa_layernorm_bwd(dy, x, weight, mean, rstd, dx, dweight=None, dbias=None, w
     w = _vec(weight, torch.float32, dim, dev, "weight")
     m, r = _vec(mean, torch.float32, rows, dev, "mean"), _vec(rstd, torch.float32, rows, dev, "rstd")
     dw, db = _vec(dweight, torch.float32, dim, dev, "dweight"), _vec(dbias, torch.float32, dim, dev, "dbias")
-    wp = _arg(ws, (torch.uint8,), None, dev, "ws")
+    wp = _ws(ws, ws_bytes, dev)
     ptrs = [dy.data_ptr(), x.data_ptr(), dx.data_ptr(), m, r]
     if rows == 0:      # empty tensors have no address, and nothing is read through one
         ptrs = [256] * 5
@@ -558,7 +565,7 @@ def dsa_dense_attn(shape, q, kv, q_pos0, kv_len, out, lse=None, ws=None, ws_byte
             _vec(q_pos0, torch.int32, B, dev, "q_pos0"), _vec(kv_len, torch.int32, B, dev, "kv_len"),
             _arg(out, _FLOATS, (B, T, H, shape.v_dim), dev, "out"),
             DSA_OUT_BF16 if out.dtype == torch.bfloat16 else DSA_OUT_F32,
-            _arg(lse, _F32, (B, T, H), dev, "lse"), _arg(ws, (torch.uint8,), None, dev, "ws"), ws_bytes)
+            _arg(lse, _F32, (B, T, H), dev, "lse"), _ws(ws, ws_bytes, dev), ws_bytes)
 
 
 def dsa_check(stream=None):

@@ -263,3 +263,15 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes(lib):
         dsa.dsa_dense_attn(s, q, kv, None, None, torch.zeros(1, 1, 128, 512))   # CPU
     with pytest.raises(ValueError):
         dsa.dsa_dense_attn(s, q, kv[:3], None, None, torch.zeros(1, 1, 128, 512))
+
+
+def test_binding_refuses_a_workspace_shorter_than_it_is_said_to_be(lib):
+    import torch
+    s = dsa.DsaShape(1, 1, 4, 64, 128, 1, 128, 576, 512, 1.0)
+    q, kv = torch.zeros(1, 1, 128, 576).bfloat16(), torch.zeros(4, 576).bfloat16()
+    out, ws = torch.zeros(1, 1, 128, 512), torch.zeros(1024, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="1024 bytes, ws_bytes is 1025"):
+        dsa.dsa_dense_attn(s, q, kv, None, None, out, ws=ws, ws_bytes=1025)
+    y, m = torch.zeros(4, 8), torch.zeros(4)
+    with pytest.raises(ValueError, match="1024 bytes, ws_bytes is 2048"):
+        dsa.dsa_layernorm_bwd(y, y, None, m, m, y, torch.zeros(8), torch.zeros(8), ws=ws, ws_bytes=2048)
