@@ -432,8 +432,9 @@ dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* view, const 
  *   x, y    [rows, dim] fp32 or bf16 each, row strides in elements
  *   weight, bias [dim] fp32, NULL = 1 and 0
  *   mean, rstd [rows] fp32, each may be NULL (the gradient needs both)
- *   1 <= dim <= 16384; y may be x (same dtype and stride), else they must not
- *   overlap; rows = 0 launches nothing. Statistics in fp32 from two passes.
+ *   1 <= dim <= 16384; y may be x (same dtype and stride), else their rows must
+ *   not overlap (columns of one buffer side by side are taken); rows = 0
+ *   launches nothing. Statistics in fp32 from two passes.
  */
 dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dtype,
                          int64_t x_stride, const float* weight, const float* bias, float eps,

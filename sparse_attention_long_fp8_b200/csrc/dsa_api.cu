@@ -844,6 +844,8 @@ dsa::RopeAngles rope_angles(const dsa_rope_spec* r) {
   return a;
 }
 
+constexpr int64_t kMaxSpan = 1ll << 46;   // elements: more than any memory, and no sum of them overflows
+
 // Bytes from the first to the end of the last element of a strided tensor.
 int64_t strided_span(const int64_t (&size)[3], const int64_t (&stride)[3], int64_t dim, int64_t esz) {
   int64_t last = dim;
@@ -1072,7 +1074,8 @@ dsa_status check_norm_tensor(const NormTensor& t, int64_t rows, int32_t dim, boo
   if (!t.p) return fail(DSA_ERR_INVALID_ARG, "%s: required pointer is NULL", t.name);
   if (t.dtype != DSA_F32 && t.dtype != DSA_BF16)
     return fail(DSA_ERR_INVALID_ARG, "%s: dtype must be DSA_F32 or DSA_BF16", t.name);
-  if (t.stride < 0 || (written && rows > 1 && t.stride < dim) || t.stride > (1ll << 40))
+  if (t.stride < 0 || (written && rows > 1 && t.stride < dim) || t.stride > (1ll << 40) ||
+      t.stride > kMaxSpan / std::max<int64_t>(rows, 1))
     return fail(DSA_ERR_INVALID_ARG, "%s: row stride %lld does not fit rows of %d", t.name,
                 static_cast<long long>(t.stride), dim);
   if (!aligned(t.p, t.dtype == DSA_BF16 ? 2 : 4))
@@ -1082,14 +1085,21 @@ dsa_status check_norm_tensor(const NormTensor& t, int64_t rows, int32_t dim, boo
 bool norm_vec(const NormTensor& t) {
   return aligned(t.p, 16) && (t.stride * (t.dtype == DSA_BF16 ? 2 : 4)) % 16 == 0;
 }
-// The written tensor is exactly the read one, or shares no byte with it.
+// The written tensor is exactly the read one, or shares no byte with it: their
+// memory is apart, or rows of one lie between the rows of the other.
 dsa_status check_norm_alias(const NormTensor& in, const NormTensor& out, int64_t rows, int32_t dim) {
   if (in.p == out.p && in.dtype == out.dtype && (in.stride == out.stride || rows <= 1)) return DSA_OK;
   const char* a = static_cast<const char*>(in.p);
   const char* b = static_cast<const char*>(out.p);
-  const int64_t na = ((std::max<int64_t>(rows, 1) - 1) * in.stride + dim) * (in.dtype == DSA_BF16 ? 2 : 4);
-  const int64_t nb = ((std::max<int64_t>(rows, 1) - 1) * out.stride + dim) * (out.dtype == DSA_BF16 ? 2 : 4);
+  const int64_t ea = in.dtype == DSA_BF16 ? 2 : 4, eb = out.dtype == DSA_BF16 ? 2 : 4;
+  const int64_t na = ((std::max<int64_t>(rows, 1) - 1) * in.stride + dim) * ea;
+  const int64_t nb = ((std::max<int64_t>(rows, 1) - 1) * out.stride + dim) * eb;
   if (a + na <= b || b + nb <= a || rows == 0) return DSA_OK;
+  const int64_t step = in.stride * ea;
+  if (step > 0 && step == out.stride * eb) {
+    const int64_t off = ((b - a) % step + step) % step;
+    if (off >= dim * ea && off + dim * eb <= step) return DSA_OK;
+  }
   return fail(DSA_ERR_INVALID_ARG, "%s overlaps %s without being the same tensor", out.name, in.name);
 }
 
@@ -1612,7 +1622,7 @@ dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* v, const voi
     return fail(DSA_ERR_INVALID_ARG, "dsa_rope: sizes must be >= 1 and dim <= 65536 (got %d, %d, %d, %d)",
                 v->batch, v->n_q, v->heads, v->dim);
   const int64_t tokens = static_cast<int64_t>(v->batch) * v->n_q;
-  if (tokens * v->heads >= (1ll << 31) || tokens >= (1ll << 31))
+  if (tokens >= (1ll << 31) || tokens * v->heads >= (1ll << 31))
     return fail(DSA_ERR_INVALID_ARG, "dsa_rope: batch * n_q * heads must be below 2^31");
   if (spec->rot_begin > v->dim - spec->rot_dim)
     return fail(DSA_ERR_INVALID_ARG, "dsa_rope: dims [%d, %d) lie outside the head's %d", spec->rot_begin,
@@ -1627,6 +1637,8 @@ dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* v, const voi
     if (v->x_stride[i] < 0 || v->out_stride[i] < 0 || v->x_stride[i] > (1ll << 40) ||
         v->out_stride[i] > (1ll << 40))
       return fail(DSA_ERR_INVALID_ARG, "dsa_rope: strides must be in [0, 2^40]");
+    if (std::max(v->x_stride[i], v->out_stride[i]) > kMaxSpan / size[i])
+      return fail(DSA_ERR_INVALID_ARG, "dsa_rope: x or out spans more than 2^46 elements");
     // the stride of a single entry plays no part
     p.xs[i] = size[i] == 1 ? 0 : v->x_stride[i];
     p.os[i] = size[i] == 1 ? 0 : v->out_stride[i];

@@ -301,6 +301,23 @@ def test_layernorm_gradient_in_place(rows, dim, dtype):
     assert torch.equal(a, want) and torch.equal(b, want)
 
 
+@pytest.mark.parametrize("rows,dim", [(300, 128), (130, 1024), (600, 4096), (37, 72)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_layernorm_between_columns_of_one_buffer(rows, dim, dtype):
+    g = _gen(dim + rows)
+    buf = _randn(g, rows, 3 * dim, dtype=dtype)
+    x, dy, w = buf[:, dim:2 * dim], buf[:, :dim], _randn(g, dim)
+    before = buf.clone()
+    mean, rstd, want = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty(rows, dim, device=DEV,
+                                                                                               dtype=dtype)
+    dsa.dsa_layernorm(x, w, None, 1e-6, want, mean, rstd)
+    dsa.dsa_layernorm(x, w, None, 1e-6, buf[:, 2 * dim:])
+    assert torch.equal(buf[:, 2 * dim:], want) and torch.equal(buf[:, :2 * dim], before[:, :2 * dim])
+    dsa.dsa_layernorm_bwd(dy, x, w, mean, rstd, want)
+    dsa.dsa_layernorm_bwd(dy, x, w, mean, rstd, buf[:, 2 * dim:])
+    assert torch.equal(buf[:, 2 * dim:], want) and torch.equal(buf[:, :2 * dim], before[:, :2 * dim])
+
+
 # ------------------------------------------------------------------ cache append
 
 def _cache(B, room, page, idx, qk, seed):

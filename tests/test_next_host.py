@@ -275,3 +275,26 @@ def test_binding_refuses_a_workspace_shorter_than_it_is_said_to_be(lib):
     y, m = torch.zeros(4, 8), torch.zeros(4)
     with pytest.raises(ValueError, match="1024 bytes, ws_bytes is 2048"):
         dsa.dsa_layernorm_bwd(y, y, None, m, m, y, torch.zeros(8), torch.zeros(8), ws=ws, ws_bytes=2048)
+
+
+# ------------------------------------------------------------------ spans
+
+def test_spans_that_would_overflow_are_refused(lib):
+    bad, big = dsa.DSA_ERR_INVALID_ARG, 1 << 30
+    huge = (big, big, 4, 128)                                          # 2^62 rows
+    assert _rope(lib, size=huge) == bad
+    assert _rope(lib, size=(1 << 20, 3, 4, 128), xs=(1 << 40, 512, 128)) == bad
+    assert _norm(lib, rows=1 << 40, xs=1 << 40, ys=1 << 40) == bad
+    assert _norm(lib, rows=1 << 20, xs=1 << 30) == bad
+
+
+def test_layernorm_takes_columns_of_one_buffer_side_by_side(lib):
+    import torch
+    bad, none = dsa.DSA_ERR_INVALID_ARG, dsa.DSA_ERR_NO_DEVICE
+    assert _norm(lib, xs=256, ys=256, y=FAKE + 2 * 127) == bad         # one column in common
+    assert _norm(lib, xs=256, ys=256, y=FAKE + 2 * 129) == bad         # the last one and the next row's first
+    assert _norm(lib, xs=512, ys=256, y=FAKE + 2 * 128) == bad         # other steps
+    if torch.cuda.is_available():
+        pytest.skip("the accepted forms are launched by the GPU tests")
+    assert _norm(lib, xs=256, ys=256, y=FAKE + 2 * 128) == none
+    assert _norm(lib, xs=384, ys=192, yd=dsa.DSA_F32, y=FAKE + 2 * 128) == none
