@@ -588,6 +588,46 @@ def test_dense_graph_replays_with_other_lengths():
     torch.cuda.current_stream().wait_stream(st)
 
 
+@pytest.mark.parametrize("lens", [[500], [513], [4000], [9473], [1000] * 4, [130, 0, 2500, 1], [1] * 7 + [3000]])
+@pytest.mark.parametrize("T", [1, 2])
+def test_dense_few_rows_in_shares_of_a_block(lens, T):
+    c = _dense_case(lens, T, 33, 128, 40 + len(lens))
+    out, lse = _dense(c)
+    _check_dense(c, out, lse, [[n - T + 1 + i for i in range(T)] for n in lens])
+
+
+def test_calls_at_once_on_two_streams():
+    """Calls that overlap on the GPU, a workspace each: the results of the same
+    calls one after another."""
+    cases = [_dense_case([3000, 77, 1500], 1, 128, 128, 51), _dense_case([700] * 40, 2, 64, 256, 52)]
+    g = _gen(53)
+    x, dy, w = _randn(g, 5000, 128, dtype=torch.bfloat16), _randn(g, 5000, 128, dtype=torch.bfloat16), _randn(g, 128)
+    mean, rstd, y = torch.empty(5000, device=DEV), torch.empty(5000, device=DEV), torch.empty_like(x)
+    dsa.dsa_layernorm(x, w, None, 1e-6, y, mean, rstd)
+    need = dsa.layernorm_bwd_workspace(5000, 128)
+    wss = [dsa.alloc_workspace(c["shape"], dsa.DSA_OP_DENSE_ATTN) for c in cases]
+    nws = [torch.empty(need, dtype=torch.uint8, device=DEV) for _ in cases]
+
+    def step(i):
+        o, l = _dense(cases[i], ws=wss[i])
+        dx, dw, db = torch.empty_like(x), torch.empty(128, device=DEV), torch.empty(128, device=DEV)
+        dsa.dsa_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, nws[i], need)
+        return o, l, dx, dw, db
+
+    want = [step(0), step(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(10):
+        got = [None, None]
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i] = step(i)
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(u, v) for u, v in zip(a, b))
+    dsa.dsa_check()
+
+
 # ------------------------------------------------------------------ together
 
 def test_serving_step_append_then_attend():
