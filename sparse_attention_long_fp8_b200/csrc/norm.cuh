@@ -495,10 +495,16 @@ struct NormRing {
     }
     __syncthreads();
   }
-  // The current stage has landed. A wait that runs out is reported; the thread
-  // goes on without waiting, so that every thread meets every barrier.
-  __device__ __forceinline__ void wait() {
-    if (ok) ok = mbar_wait(&full[st], phase);
+  // The current stage, of row r, has landed. A wait that runs out is reported; the
+  // thread waits once more for every copy in flight, issues none any more and goes
+  // on without waiting, so that every thread meets every barrier.
+  __device__ __forceinline__ void wait(long long r, long long step, long long rows) {
+    if (!ok) return;
+    ok = mbar_wait(&full[st], phase);
+    if (ok) return;
+#pragma unroll 1
+    for (int k = 0; k < stages && r + k * step < rows; ++k)
+      mbar_wait(&full[st + k < stages ? st + k : st + k - stages], st + k < stages ? phase : phase ^ 1);
   }
   __device__ __forceinline__ void next() {
     if (++st == stages) {
@@ -537,7 +543,7 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, false)) norm_wide_ker
   const float inv = 1.0f / static_cast<float>(p.dim);
   for (long long r = blockIdx.x; r < p.rows; r += step) {
     float x[EPT], s[1] = {0.f}, q[1] = {0.f};
-    ring.wait();
+    ring.wait(r, step, p.rows);
     {
       Row raw;
       raw.load(ring.data + ring.st * bytes, 0, p.x_bf16, lane, p.dim);
@@ -546,7 +552,7 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, false)) norm_wide_ker
 #pragma unroll
     for (int j = 0; j < EPT; ++j) s[0] += x[j];
     norm_sums<TPR, 1>(s, slots, buf);
-    if (lane == 0) copy_in(r + stages * step, ring.st);
+    if (lane == 0 && ring.ok) copy_in(r + stages * step, ring.st);
     ring.next();
     const float mean = s[0] * inv;
 #pragma unroll
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, true))
     const float mean = nmean, rstd = nrstd;
     stats(r + step);
     float x[EPT], d[EPT], s[2] = {0.f, 0.f};
-    ring.wait();
+    ring.wait(r, step, p.rows);
     {
       const uint8_t* src = ring.data + ring.st * (x_bytes + dy_bytes);
       Row raw;
@@ -641,7 +647,7 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, true))
       s[1] = fmaf(d[j], x[j], s[1]);
     }
     norm_sums<TPR, 2>(s, slots, buf);
-    if ((lane & 31) == 0 && warp < 2) copy_in(r + stages * step, ring.st, warp);
+    if ((lane & 31) == 0 && warp < 2 && ring.ok) copy_in(r + stages * step, ring.st, warp);
     ring.next();
     const float mg = s[0] * inv, mgx = s[1] * inv;
 #pragma unroll
