@@ -890,8 +890,13 @@ bool rows_apart(const void* x, const int64_t (&xs)[3], const void* out, const in
 
 template <class T, int E>
 void launch_rope_t(const dsa::RopeParams& p, unsigned grid, int smem, cudaStream_t st) {
-  if (p.a.half) dsa::rope_kernel<T, E, true><<<grid, dsa::kRopeThreads, smem, st>>>(p);
-  else dsa::rope_kernel<T, E, false><<<grid, dsa::kRopeThreads, smem, st>>>(p);
+  if constexpr (E == 1 || E * sizeof(T) == 16) {
+    if (!p.a.half) {
+      dsa::rope_kernel<T, E, false><<<grid, dsa::kRopeThreads, smem, st>>>(p);
+      return;
+    }
+  }
+  dsa::rope_kernel<T, E, true><<<grid, dsa::kRopeThreads, smem, st>>>(p);
 }
 
 // ------------------------------------------------------------------ layer norm
@@ -1660,32 +1665,41 @@ dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* v, const voi
   p.by_heads = dsa::FastDiv::make(static_cast<uint32_t>(v->heads));
   p.by_tokens = dsa::FastDiv::make(static_cast<uint32_t>(v->n_q));
   p.a = rope_angles(spec);
-  // 16-byte chunks when every chunk of every row starts on one
-  const int e = 16 / esz;
-  bool vec = aligned(x, 16) && aligned(out, 16) && p.a.begin % e == 0 &&
-             (p.a.half ? p.a.pairs : 2 * p.a.pairs) % e == 0 && (same || v->dim % e == 0);
-  for (int i = 0; i < 3; ++i) vec = vec && p.xs[i] % e == 0 && p.os[i] % e == 0;
+  // The longest chunks, up to 16 bytes, that every chunk of every row starts on
+  // (halves, 8192 x 64 rows of 68 bf16: 44 us by 8 bytes, 69 by single elements).
+  // Interleaved pairs: 16 bytes or single elements (802 K rows of 102 bf16: 131 us
+  // by single elements, eight rows at a time, 222 by pairs of 4 bytes, four rows).
+  int e = 16 / esz;
+  for (; e > 1; e /= 2) {
+    bool fits = aligned(x, e * esz) && aligned(out, e * esz) && p.a.begin % e == 0 &&
+                (p.a.half ? p.a.pairs : 2 * p.a.pairs) % e == 0 && (same || v->dim % e == 0);
+    for (int i = 0; i < 3; ++i) fits = fits && p.xs[i] % e == 0 && p.os[i] % e == 0;
+    if (fits && (p.a.half || e == 16 / esz)) break;
+  }
   // Rows per CTA: what its threads hold in one unrolled step, times up to
   // four while every SM keeps several CTAs; fewer when the tokens' cos and sin
   // would not fit (one token more than the rows' share may be touched at each end).
-  const int per_item = vec ? (p.a.half ? e : e / 2) : 1;
+  const int per_item = p.a.half ? e : std::max(e / 2, 1);
   const int lanes = std::max(1, dsa::kRopeThreads / (p.a.pairs / per_item));
   const int64_t cap = std::min<int64_t>(dsa::kRopeMaxTokens, dsa::kRopeTableBytes / (8 * p.a.pairs));
   int64_t per_cta = lanes;
   while (per_cta < 16 * lanes && p.rows / (2 * per_cta) >= 8ll * num_sms()) per_cta *= 2;
   per_cta = std::max<int64_t>(1, std::min(per_cta, (cap - 2) * v->heads));
-  p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(per_cta, 1 << 20));
+  p.rows_per_cta = static_cast<int32_t>(std::min<int64_t>(per_cta, dsa::kRopeMaxRows));
   const int64_t touched = std::min<int64_t>(tokens, (p.rows_per_cta - 1) / v->heads + 2);
-  const int smem = static_cast<int>(touched * p.a.pairs * 8);
+  const int smem = dsa::rope_smem(e * esz, p.rows_per_cta, static_cast<int>(touched), p.a.pairs);
   const unsigned grid = (p.rows + p.rows_per_cta - 1) / static_cast<uint32_t>(p.rows_per_cta);
   int dev;
   if (dsa_status st = current_device(&dev)) return st;
   cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   if (v->dtype == DSA_BF16) {
-    if (vec) launch_rope_t<__nv_bfloat16, 8>(p, grid, smem, st_);
+    if (e == 8) launch_rope_t<__nv_bfloat16, 8>(p, grid, smem, st_);
+    else if (e == 4) launch_rope_t<__nv_bfloat16, 4>(p, grid, smem, st_);
+    else if (e == 2) launch_rope_t<__nv_bfloat16, 2>(p, grid, smem, st_);
     else launch_rope_t<__nv_bfloat16, 1>(p, grid, smem, st_);
   } else {
-    if (vec) launch_rope_t<float, 4>(p, grid, smem, st_);
+    if (e == 4) launch_rope_t<float, 4>(p, grid, smem, st_);
+    else if (e == 2) launch_rope_t<float, 2>(p, grid, smem, st_);
     else launch_rope_t<float, 1>(p, grid, smem, st_);
   }
   DSA_CUDA_TRY(cudaGetLastError(), "rotary positions launch");

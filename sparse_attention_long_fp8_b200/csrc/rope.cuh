@@ -12,9 +12,14 @@
 // all heads of the CTA's rows.
 //
 // Bound: HBM, one read and one write per element (in place: of the rotated
-// part only). Threads move 16-byte chunks when every address allows it (the
-// rotated part's halves and the strides are multiples of a chunk), single
-// elements otherwise; several rows are loaded before the first is turned.
+// part only): 16384 x 64 heads of 128 bf16 in 91.5 us, 5.87 TB/s. Threads move the
+// longest chunks, up to 16 bytes, that every address allows (the rotated part's
+// halves and the strides are multiples of one; interleaved pairs: 16 bytes or
+// single elements); several rows are loaded before the first is turned. Rows at
+// odd addresses are bound by sectors written in parts and by how little single
+// elements keep on its way: 8192 x 64 rows of 133 bf16 in 89 us, 3.1 TB/s (116 us
+// with every thread forming its rows' offsets and four rows on their way; 219 us
+// with a thread per element, whose stores would be whole but whose loads double).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,11 +30,20 @@ namespace dsa {
 
 constexpr int kRopeMaxPairs = 128;
 constexpr int kRopeThreads = 256;
-constexpr int kRopeTableBytes = 32768;   // cos / sin of one CTA's tokens
-constexpr int kRopeMaxTokens = 512;      // tokens of one CTA
-// Rows a thread loads before it turns any: 64 bytes of 16-byte chunks.
-template <int E, bool HALF>
-constexpr int rope_unroll() { return HALF && E > 1 ? 2 : 4; }
+// Shared memory of one CTA: below 48 KB with both at their largest.
+constexpr int kRopeTableBytes = 28672;   // cos / sin of its tokens
+constexpr int kRopeMaxRows = 1024;       // its rows: offsets and token of each
+constexpr int kRopeMaxTokens = 512;
+// Chunks below 16 bytes: many per row, so a row's offsets are formed once.
+constexpr bool rope_rows_in_smem(int bytes) { return bytes < 16; }
+constexpr int rope_smem(int bytes, int rows, int tokens, int pairs) {
+  return (rope_rows_in_smem(bytes) ? rows * 18 : 0) + tokens * pairs * 8;
+}
+// Rows a thread loads before it turns any: 64 bytes of 16-byte chunks, 4 rows of
+// shorter chunks, 8 of single elements, which would else leave too little on its
+// way (8192 x 64 rows of 133 bf16: 89 us, 92 with 4 rows, 127 with 12).
+template <int E, int BYTES, bool HALF>
+constexpr int rope_unroll() { return BYTES == 16 ? (HALF ? 2 : 4) : E == 1 ? 8 : 4; }
 
 // One rotation as the kernels take it (from dsa_rope_spec).
 struct RopeAngles {
@@ -110,23 +124,40 @@ struct alignas(E * sizeof(T)) RopeChunk {
   T v[E];
 };
 
-// E elements per chunk: 16 bytes of T, or 1. An item is E pairs (half: a chunk
-// of each half) or max(E / 2, 1) pairs (interleaved: one chunk, or two
-// neighbouring elements).
+// E elements per chunk. An item is E pairs (half: a chunk of each half) or
+// max(E / 2, 1) pairs (interleaved: one chunk, or two neighbouring elements).
 template <class T, int E, bool HALF>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
-  constexpr int kUnroll = rope_unroll<E, HALF>();
+  constexpr int kUnroll = rope_unroll<E, E * sizeof(T), HALF>();
   constexpr int HP = HALF ? E : (E > 1 ? E / 2 : 1);
   using Chunk = RopeChunk<T, E>;
-  extern __shared__ float2 cs[];                       // [tokens][pairs]
+  constexpr bool ROWS = rope_rows_in_smem(E * sizeof(T));
+  extern __shared__ __align__(16) uint8_t rope_smem_base[];
+  longlong2* const offs = reinterpret_cast<longlong2*>(rope_smem_base);       // [rows] x, out
+  float2* const cs = reinterpret_cast<float2*>(offs + (ROWS ? p.rows_per_cta : 0));   // [tokens][pairs]
   __shared__ double turns[kRopeMaxPairs];
   __shared__ uint8_t live[kRopeMaxTokens];
   const int P = p.a.pairs;
   const uint32_t row0 = blockIdx.x * static_cast<uint32_t>(p.rows_per_cta);
-  const uint32_t row1 = min(row0 + static_cast<uint32_t>(p.rows_per_cta), p.rows);
+  const int nrow = static_cast<int>(min(static_cast<uint32_t>(p.rows_per_cta), p.rows - row0));
   const uint32_t tok0 = p.by_heads.div(row0);
-  const int ntok = static_cast<int>(p.by_heads.div(row1 - 1) - tok0) + 1;
+  const int ntok = static_cast<int>(p.by_heads.div(row0 + nrow - 1) - tok0) + 1;
+  int16_t* const token = reinterpret_cast<int16_t*>(cs + ntok * P);           // [rows]
+  auto place = [&](int i, int64_t& xo, int64_t& oo) -> int {
+    const uint32_t row = row0 + i, tok = p.by_heads.div(row), b = p.by_tokens.div(tok);
+    const int64_t h = row - tok * static_cast<uint32_t>(p.heads);
+    const int64_t t = tok - b * static_cast<uint32_t>(p.n_q);
+    xo = b * p.xs[0] + t * p.xs[1] + h * p.xs[2];
+    oo = b * p.os[0] + t * p.os[1] + h * p.os[2];
+    return static_cast<int>(tok - tok0);
+  };
   for (int i = threadIdx.x; i < P; i += kRopeThreads) turns[i] = p.a.turns[i];
+  if constexpr (ROWS)
+    for (int i = threadIdx.x; i < nrow; i += kRopeThreads) {
+      int64_t xo, oo;
+      token[i] = static_cast<int16_t>(place(i, xo, oo));
+      offs[i] = make_longlong2(xo, oo);
+    }
   __syncthreads();
   for (int i = threadIdx.x; i < ntok * P; i += kRopeThreads) {
     const int tk = i / P, pr = i - tk * P;
@@ -142,18 +173,25 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
 
   const T* x = static_cast<const T*>(p.x);
   T* out = static_cast<T*>(p.out);
-  // Offsets of a row in x and out; -1 for a row past the end or a padding token.
-  auto locate = [&](uint32_t row, int64_t& xo, int64_t& oo, int& tk) -> bool {
-    if (row >= row1) return false;
-    const uint32_t tok = p.by_heads.div(row);
-    tk = static_cast<int>(tok - tok0);
-    if (!live[tk]) return false;
-    const int64_t h = row - tok * static_cast<uint32_t>(p.heads);
-    const uint32_t b = p.by_tokens.div(tok);
-    const int64_t t = tok - b * static_cast<uint32_t>(p.n_q);
-    xo = b * p.xs[0] + t * p.xs[1] + h * p.xs[2];
-    oo = b * p.os[0] + t * p.os[1] + h * p.os[2];
+  // Offset in x of the CTA's row i; false past the end and for padding. The
+  // offset in out and the token are kept beside it, or (ROWS) looked up again.
+  auto locate = [&](int i, int64_t& xo, int64_t& oo, int& tk) -> bool {
+    if (i >= nrow) return false;
+    if constexpr (ROWS) {
+      if (!live[token[i]]) return false;
+      xo = offs[i].x;
+    } else {
+      tk = static_cast<int>(p.by_heads.div(row0 + i) - tok0);
+      if (!live[tk]) return false;
+      place(i, xo, oo);
+    }
     return true;
+  };
+  auto target = [&](int i, int64_t& oo, int& tk) {
+    if constexpr (ROWS) {
+      tk = token[i];
+      oo = offs[i].y;
+    }
   };
 
   {
@@ -163,7 +201,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
     const int first = p.a.begin + (HALF ? item * E : 2 * item * HP);
     const int second = HALF ? first + P : first + 1;   // second: halves, or the scalar neighbour
     if (ry < lanes)
-      for (uint32_t r = row0 + ry; r < row1; r += lanes * kUnroll) {
+      for (int r = ry; r < nrow; r += lanes * kUnroll) {
         Chunk u[kUnroll], w[kUnroll];
         int64_t oo[kUnroll];
         int tk[kUnroll];
@@ -180,6 +218,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < kUnroll; ++k) {
           if (!on[k]) continue;
+          target(r + k * lanes, oo[k], tk[k]);
           const float2* t = cs + tk[k] * P + item * HP;
 #pragma unroll
           for (int j = 0; j < HP; ++j) {
@@ -211,15 +250,15 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   for (int c = c0; c < chunks; c += 2 * wide) {
     const bool two = c + wide < chunks;
     const int e0 = at(c), e1 = at(two ? c + wide : c);
-    for (uint32_t r = row0 + ry; r < row1; r += lanes * kUnroll) {
+    for (int r = ry; r < nrow; r += lanes * kUnroll) {
       Chunk u[kUnroll], w[kUnroll];
       int64_t oo[kUnroll];
+      int tk[kUnroll];
       bool on[kUnroll];
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k) {
         int64_t xo;
-        int tk;
-        on[k] = locate(r + k * lanes, xo, oo[k], tk);
+        on[k] = locate(r + k * lanes, xo, oo[k], tk[k]);
         if (on[k]) {
           u[k] = *reinterpret_cast<const Chunk*>(x + xo + e0);
           w[k] = *reinterpret_cast<const Chunk*>(x + xo + e1);
@@ -228,6 +267,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
 #pragma unroll
       for (int k = 0; k < kUnroll; ++k)
         if (on[k]) {
+          target(r + k * lanes, oo[k], tk[k]);
           *reinterpret_cast<Chunk*>(out + oo[k] + e0) = u[k];
           if (two) *reinterpret_cast<Chunk*>(out + oo[k] + e1) = w[k];
         }

@@ -98,6 +98,31 @@ def test_rope(B, T, H, D, rot, begin, layout, dtype):
         assert torch.equal(y, out)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", [dsa.DSA_ROPE_HALF, dsa.DSA_ROPE_INTERLEAVED])
+@pytest.mark.parametrize("B,T,H,D,rot,begin,width,lead", [
+    (2, 33, 3, 36, 20, 8, 36, 0), (1, 700, 2, 38, 28, 6, 44, 2), (3, 129, 5, 60, 44, 4, 124, 4),
+    (2, 257, 64, 40, 24, 12, 48, 4), (1, 1500, 1, 31, 26, 0, 95, 1), (2, 40, 97, 150, 126, 8, 151, 0),
+    (64, 3, 1, 8, 8, 0, 10, 2), (1, 5000, 3, 9, 2, 3, 9, 0)])
+def test_rope_at_every_alignment(B, T, H, D, rot, begin, width, lead, layout, dtype):
+    g = _gen(T + D)
+    x = _randn(g, B, T, H, D, dtype=dtype)
+    wide = torch.full((B, T, H, width), 7.0, device=DEV, dtype=dtype)
+    out = wide[..., lead:lead + D]
+    pos = torch.randint(0, 9000, (B, T), generator=g, device=DEV, dtype=torch.int32)
+    pad = torch.rand(B, T, generator=g, device=DEV) < 0.1
+    spec = dsa.rope_spec(rot, rot_begin=begin, layout=layout)
+    dsa.dsa_rope(spec, x, out, row_pos=torch.where(pad, -1, pos).to(torch.int32))
+    want, size = _turn64(x, pos, spec, False)
+    want[pad], size[pad] = 7.0, 0.0
+    _within(out, want, _rope_tol(want, size, dtype), "rope")
+    assert (wide[..., :lead] == 7.0).all() and (wide[..., lead + D:] == 7.0).all()
+    y = torch.full_like(wide, 3.0)[..., lead:lead + D]
+    y.copy_(x)
+    dsa.dsa_rope(spec, y, y, row_pos=torch.where(pad, -1, pos).to(torch.int32))    # in place
+    assert torch.equal(y[~pad], out[~pad]) and torch.equal(y[pad], x[pad])
+
+
 @pytest.mark.parametrize("pos", [0, 1, 1 << 20, (1 << 31) - 2])
 def test_rope_far_positions(pos):
     g = _gen(3)
