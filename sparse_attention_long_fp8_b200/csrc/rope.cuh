@@ -55,21 +55,24 @@ struct RopeAngles {
 
 // (A cos, A sin) of pos positions at `turns` turns per position. The fraction of
 // a turn, in [-1/2, 1/2], is cut to the nearest quarter q and a rest of at most
-// 1/8, x = 2 pi rest in [-pi/4, pi/4]; sin x and cos x by their Taylor series (the
-// first terms left out are below x^11 / 11! = 2e-9 and x^10 / 10! = 3e-8), turned
-// by q quarters. Off by at most about 2^-23 with the rounding of the fraction.
+// 1/8, x = 2 pi rest in [-pi/4, pi/4], in fp64 up to the one rounding of x; sin x
+// and cos x by their Taylor series (the first terms left out are below
+// x^11 / 11! = 2e-9 and x^12 / 12! = 2e-10), turned by q quarters. Off by about an
+// ulp. (With the fraction itself rounded to fp32 the angle is off by up to 1e-7: of
+// 80 M appended E4M3 codes 148 instead of 121 miss the 64-bit formula's; a form with
+// cos and sin rounded from 64 bits misses 128.)
 __device__ __forceinline__ float2 rope_cos_sin(double turns, int pos, float amplitude) {
   double t = static_cast<double>(pos) * turns;
   t -= rint(t);
-  const float f = static_cast<float>(t);
-  const float qf = rintf(4.0f * f);
-  const float x = 6.28318531f * fmaf(-0.25f, qf, f);          // the difference is exact
+  const float qf = rintf(4.0f * static_cast<float>(t));
+  const float x = static_cast<float>(fma(-0.25, static_cast<double>(qf), t) * 6.283185307179586);
   const float x2 = x * x;
   float s = fmaf(x2, 1.0f / 362880.0f, -1.0f / 5040.0f);
   s = fmaf(x2, s, 1.0f / 120.0f);
   s = fmaf(x2, s, -1.0f / 6.0f);
   s = fmaf(x2 * s, x, x);
-  float c = fmaf(x2, 1.0f / 40320.0f, -1.0f / 720.0f);
+  float c = fmaf(x2, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  c = fmaf(x2, c, -1.0f / 720.0f);
   c = fmaf(x2, c, 1.0f / 24.0f);
   c = fmaf(x2, c, -0.5f);
   c = fmaf(x2, c, 1.0f);
