@@ -5,10 +5,10 @@
 // halves' elements i and i + rot/2 (half layout) or neighbours 2i and 2i + 1
 // (interleaved).
 //
-// The angle is formed in turns, pos * (freq / 2 pi), in fp64 and only its
-// fraction goes on in fp32: at position 2^20 an fp32 product would be off by
-// 2^-4 radians, the fraction is off by 2^-25 turns at any position. Every
-// (token, pair) is evaluated once per CTA, into shared memory, and used by
+// The angle is formed in turns, pos * (freq / 2 pi), in fp64 and reduced there to
+// an eighth of a turn, which goes on in fp32: at position 2^20 an fp32 product
+// would be off by 2^-4 radians, the reduced angle is off by 2^-25 at any position.
+// Every (token, pair) is evaluated once per CTA, into shared memory, and used by
 // all heads of the CTA's rows.
 //
 // Bound: HBM, one read and one write per element (in place: of the rotated
