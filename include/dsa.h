@@ -447,7 +447,10 @@ dsa_status dsa_layernorm(int64_t rows, int32_t dim, const void* x, int32_t x_dty
  *   dy xh, dbias = sum over rows of dy (zeros for rows = 0).
  *   dy, x, dx [rows, dim] fp32 or bf16 each; dx may be dy or x (same dtype
  *   and stride). weight NULL = 1. dweight and dbias [dim] fp32 may be NULL.
- *   The row sums are fp32, in a fixed order: the same bits on every call.
+ *   The row sums are fp32, in a fixed order: the same bits on every call. Rows
+ *   of up to four values are formed in fp64, from mean and rstd as given: on
+ *   rows of two, dx is (eps rstd^2) of its terms, so what rounding of rstd or
+ *   mean to fp32 the forward made shows in it, 2^-23 / (eps rstd^2) of dx.
  *   Workspace: dsa_layernorm_bwd_workspace bytes, 16-byte aligned (none is
  *   needed when dweight and dbias are both NULL). Calls that may overlap on
  *   the GPU need a workspace each.

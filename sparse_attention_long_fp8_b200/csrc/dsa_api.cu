@@ -934,6 +934,9 @@ unsigned norm_grid(int64_t rows, int dim, bool gradient, bool wide) {
   int64_t groups = 1;
   if (wide) {
     per_sm = dsa::norm_wide_ctas(norm_wide_tpr(dim, gradient), gradient);
+  } else if (gradient && dim <= dsa::kNormFewDim) {
+    groups = dsa::kNormFewThreads;
+    per_sm = dsa::kNormFewCtas;
   } else {
     const int tpr = norm_pick(dim).tpr;
     groups = norm_groups(tpr);
@@ -1040,6 +1043,10 @@ dsa_status launch_norm_bwd(const dsa::NormBwdParams& p, bool vec, cudaStream_t s
     case 512: return launch_norm_bwd_wide_t<512, 2>(p, grid, st, dev);
     case 1024: return launch_norm_bwd_wide_t<1024, 2>(p, grid, st, dev);
     default: break;
+  }
+  if (p.dim <= dsa::kNormFewDim) {
+    dsa::norm_bwd_few_kernel<<<grid, dsa::kNormFewThreads, 0, st>>>(p);
+    return DSA_OK;
   }
   const NormPick k = norm_pick(p.dim);
   switch ((k.tpr * 8 + k.nv) * 2 + vec) {

@@ -8,7 +8,8 @@
 // Bound: HBM, each row read once and written once. A row stays in registers
 // between its passes (two passes for the variance: sum of squares minus
 // squared mean would cancel in fp32 when |mean| >> sigma). TPR threads share a
-// row and hold 8 NV elements each. All arithmetic is fp32; bf16 only at loads and stores.
+// row and hold 8 NV elements each. Arithmetic is fp32 but for the gradient of rows of
+// up to four values; bf16 only at loads and stores.
 //
 // The weight's gradient: a thread keeps the sums of its columns over all the
 // rows its CTA walks, the CTA writes one partial row, and a second kernel adds
@@ -428,6 +429,77 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
         part[p.dim + e] = ab[j];
       }
     }
+  }
+}
+
+// ---------------------------------------------------------------- rows of a few values
+
+// The gradient of rows of at most kNormFewDim values, a thread per row in fp64.
+// dx is what g keeps without its parts along 1 and xh, and xh is orthogonal to 1, so
+// rows of two values keep next to nothing of it: dx = rstd (g1 - g2) / 2 (1 - xh^2)
+// with 1 - xh^2 = eps rstd^2, 1e-6 and less, which the rounding of xh to fp32
+// (2^-24) buries: of 200 K such rows the median was off by 6 %. Rows of three or
+// four values lose the digits where g happens to lie near the two directions (3 in
+// 1000 and 1 in 100000 off by more than 2e-5), rows of five no longer (none). fp64
+// costs nothing here: the time is the launch's and, for many rows, HBM's.
+constexpr int kNormFewDim = 4, kNormFewThreads = 256, kNormFewCtas = 2;
+
+__device__ __forceinline__ double norm_elem(const void* base, long long at, int bf16) {
+  return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]) : static_cast<const float*>(base)[at];
+}
+
+__global__ void __launch_bounds__(kNormFewThreads, kNormFewCtas) norm_bwd_few_kernel(const NormBwdParams p) {
+  constexpr int D = kNormFewDim, WARPS = kNormFewThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double w[D], acc[2][D];          // acc: this thread's rows' dweight, dbias
+#pragma unroll
+  for (int j = 0; j < D; ++j) {
+    w[j] = p.w && j < p.dim ? p.w[j] : 1.f;
+    acc[0][j] = acc[1][j] = 0.0;
+  }
+  const double inv = 1.0 / p.dim;
+  const long long step = static_cast<long long>(gridDim.x) * kNormFewThreads;
+  for (long long r = static_cast<long long>(blockIdx.x) * kNormFewThreads + threadIdx.x; r < p.rows; r += step) {
+    const double mean = p.mean[r], rstd = p.rstd[r];
+    double h[D], g[D], sg = 0.0, sgx = 0.0;
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      if (j >= p.dim) continue;
+      const double d = norm_elem(p.dy, r * p.dys + j, p.dy_bf16);
+      h[j] = (norm_elem(p.x, r * p.xs + j, p.x_bf16) - mean) * rstd;
+      acc[0][j] = fma(d, h[j], acc[0][j]);
+      acc[1][j] += d;
+      g[j] = d * w[j];
+      sg += g[j];
+      sgx = fma(g[j], h[j], sgx);
+    }
+    const double mg = sg * inv, mgx = sgx * inv;
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      if (j >= p.dim) continue;
+      const float dx = static_cast<float>(rstd * (g[j] - mg - h[j] * mgx));
+      if (p.dx_bf16) static_cast<__nv_bfloat16*>(p.dx)[r * p.dxs + j] = __float2bfloat16_rn(dx);
+      else static_cast<float*>(p.dx)[r * p.dxs + j] = dx;
+    }
+  }
+  griddep_launch_dependents();
+  if (!p.part) return;
+  __shared__ double sums[WARPS][2 * D];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < D; ++j) {
+      double v = acc[k][j];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) sums[warp][k * D + j] = v;
+    }
+  __syncthreads();
+  if (threadIdx.x < 2 * D && threadIdx.x % D < p.dim) {
+    double v = 0.0;
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) v += sums[i][threadIdx.x];
+    p.part[(static_cast<size_t>(blockIdx.x) * 2 + threadIdx.x / D) * p.dim + threadIdx.x % D] = static_cast<float>(v);
   }
 }
 

@@ -1,0 +1,55 @@
+"""Edges of the operators next to the sparse path: rows of a few values, values
+that are not finite, positions far out. Tolerances count roundings as in
+test_gpu_next.py."""
+import math
+
+import pytest
+import torch
+
+import sparse_attention_long_fp8_b200 as dsa
+from test_gpu_next import (DEV, HALF, U, _cache, _check_dense, _clean, _dense, _dense_case, _gen,  # noqa: F401
+                           _norm64, _randn, _rope_tol, _turn64, _within)
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ layer norm
+
+@pytest.mark.parametrize("xt,gt,dt", [(torch.bfloat16, torch.float32, torch.bfloat16),
+                                      (torch.float32, torch.float32, torch.float32),
+                                      (torch.float32, torch.bfloat16, torch.float32)])
+@pytest.mark.parametrize("rows", [1, 3, 257, 90001])
+@pytest.mark.parametrize("dim", [1, 2, 3, 4])
+def test_layernorm_gradient_of_rows_of_a_few_values(dim, rows, xt, gt, dt):
+    """dx of rows of two values is a millionth of its terms (1 - hat^2 = eps
+    rstd^2): it has to be right relative to itself."""
+    g = _gen(rows * 5 + dim)
+    wide = (_randn(g, rows, dim + 3) * 2 + 0.5).to(xt)
+    x, dy, w = wide[:, 1:1 + dim], _randn(g, rows, dim, dtype=gt), 1 + 0.2 * _randn(g, dim)
+    m, r, _ = _norm64(x, 1e-6)
+    mean, rstd = m[:, 0].float(), r[:, 0].float()
+    n = dsa.layernorm_bwd_workspace(rows, dim)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    hat = (x.double() - mean.double()[:, None]) * rstd.double()[:, None]
+    d = dy.double()
+    for weight in (w, None):
+        dx = torch.empty(rows, dim, device=DEV, dtype=dt)
+        dw, db = torch.full((dim,), 9.0, device=DEV), torch.full((dim,), 9.0, device=DEV)
+        dsa.dsa_layernorm_bwd(dy, x, weight, mean, rstd, dx, dw, db, ws, n)
+        q = d * (weight.double() if weight is not None else 1.0)
+        want = rstd.double()[:, None] * (q - q.mean(-1, keepdim=True) - hat * (q * hat).mean(-1, keepdim=True))
+        size = rstd.double()[:, None] * (q.abs() + q.abs().mean(-1, keepdim=True)
+                                         + hat.abs() * (q * hat).abs().mean(-1, keepdim=True))
+        # at most 16 roundings of 2^-53 on either side; one to fp32, one to dx's type
+        lost = size * 32 * 2.0 ** -53
+        _within(dx, want, lost + (want.abs() + lost) * (HALF[dt] + 2 * U), "dx")
+        # fp64 within a CTA; at most 352 partial rows, 11 in a thread and 32 + 5 sums after that
+        _within(dw, (d * hat).sum(0), (d * hat).abs().sum(0) * 64 * U, "dweight")
+        _within(db, d.sum(0), d.abs().sum(0) * 64 * U, "dbias")
+    dx2, dw2, db2 = torch.empty_like(dx), torch.empty_like(dw), torch.empty_like(db)
+    dsa.dsa_layernorm_bwd(dy, x, None, mean, rstd, dx2, dw2, db2, ws, n)
+    assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and torch.equal(db, db2)      # the same bits
+    if dt == gt:
+        a = dy.clone()
+        dsa.dsa_layernorm_bwd(a, x, None, mean, rstd, a)                               # in place
+        assert torch.equal(a, dx)
