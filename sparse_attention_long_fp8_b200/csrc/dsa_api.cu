@@ -973,18 +973,24 @@ void launch_norm_t(const dsa::NormParams& p, unsigned grid, cudaStream_t st) {
     norm_kernel<VEC, TPR, NV, kRowAny><<<grid, threads, 0, st>>>(p);
   }
 }
-template <bool VEC, int TPR, int NV>
-void launch_norm_bwd_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
+template <bool VEC, bool PADS, int TPR, int NV>
+void launch_norm_bwd_p(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
   using namespace dsa;
   constexpr int threads = norm_threads<TPR>();
   if constexpr (VEC && NV == 1) {
-    if (p.x_bf16 && p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowBf16><<<grid, threads, 0, st>>>(p);
-    else if (p.x_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowBf16, kRowF32><<<grid, threads, 0, st>>>(p);
-    else if (p.dy_bf16) norm_bwd_kernel<VEC, TPR, NV, kRowF32, kRowBf16><<<grid, threads, 0, st>>>(p);
-    else norm_bwd_kernel<VEC, TPR, NV, kRowF32, kRowF32><<<grid, threads, 0, st>>>(p);
+    if (p.x_bf16 && p.dy_bf16) norm_bwd_kernel<VEC, PADS, TPR, NV, kRowBf16, kRowBf16><<<grid, threads, 0, st>>>(p);
+    else if (p.x_bf16) norm_bwd_kernel<VEC, PADS, TPR, NV, kRowBf16, kRowF32><<<grid, threads, 0, st>>>(p);
+    else if (p.dy_bf16) norm_bwd_kernel<VEC, PADS, TPR, NV, kRowF32, kRowBf16><<<grid, threads, 0, st>>>(p);
+    else norm_bwd_kernel<VEC, PADS, TPR, NV, kRowF32, kRowF32><<<grid, threads, 0, st>>>(p);
   } else {
-    norm_bwd_kernel<VEC, TPR, NV, kRowAny, kRowAny><<<grid, threads, 0, st>>>(p);
+    norm_bwd_kernel<VEC, PADS, TPR, NV, kRowAny, kRowAny><<<grid, threads, 0, st>>>(p);
   }
+}
+template <bool VEC, int TPR, int NV>
+void launch_norm_bwd_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st) {
+  if constexpr (VEC)
+    if (p.dim == 8 * NV * TPR) return launch_norm_bwd_p<VEC, false, TPR, NV>(p, grid, st);
+  launch_norm_bwd_p<VEC, true, TPR, NV>(p, grid, st);
 }
 template <int TPR, int NV>
 dsa_status launch_norm_wide_t(const dsa::NormParams& p, unsigned grid, cudaStream_t st, int dev) {
@@ -995,14 +1001,19 @@ dsa_status launch_norm_wide_t(const dsa::NormParams& p, unsigned grid, cudaStrea
   dsa::norm_wide_kernel<TPR, NV><<<grid, TPR, 128 + stages * bytes, st>>>(p, stages);
   return DSA_OK;
 }
-template <int TPR, int NV>
-dsa_status launch_norm_bwd_wide_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st, int dev) {
+template <int TPR, int NV, bool PADS>
+dsa_status launch_norm_bwd_wide_p(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st, int dev) {
   static std::atomic<bool> attr_done[kMaxDevices];
-  if (dsa_status e = set_smem(dsa::norm_bwd_wide_kernel<TPR, NV>, kNormMaxSmem, dev, attr_done)) return e;
+  if (dsa_status e = set_smem(dsa::norm_bwd_wide_kernel<TPR, NV, PADS>, kNormMaxSmem, dev, attr_done)) return e;
   const size_t bytes = static_cast<size_t>(p.dim) * ((p.x_bf16 ? 2 : 4) + (p.dy_bf16 ? 2 : 4));
   const int stages = norm_stages(dsa::norm_wide_ctas(TPR, true), bytes);
-  dsa::norm_bwd_wide_kernel<TPR, NV><<<grid, TPR, 128 + stages * bytes, st>>>(p, stages);
+  dsa::norm_bwd_wide_kernel<TPR, NV, PADS><<<grid, TPR, 128 + stages * bytes, st>>>(p, stages);
   return DSA_OK;
+}
+template <int TPR, int NV>
+dsa_status launch_norm_bwd_wide_t(const dsa::NormBwdParams& p, unsigned grid, cudaStream_t st, int dev) {
+  return p.dim == 8 * NV * TPR ? launch_norm_bwd_wide_p<TPR, NV, false>(p, grid, st, dev)
+                               : launch_norm_bwd_wide_p<TPR, NV, true>(p, grid, st, dev);
 }
 
 dsa_status launch_norm(const dsa::NormParams& p, bool vec, cudaStream_t st, int dev) {

@@ -310,6 +310,16 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::
   }
 }
 
+// Whether the places past a row's end, which hold (0 - mean) rstd and are multiplied
+// by 0, would overflow to infinity and make their products NaN: rows of equal values
+// past 1e35, say. Such a row's sum is formed again without them. PADS: compiled
+// only into the kernels of rows that leave places empty, as the branch alone costs
+// registers (8191 fp32 rows of 4096: 70.0 us, 72.9 with it, 80.8 with a test at
+// every place).
+__device__ __forceinline__ bool norm_pads_overflow(float mean, float rstd) {
+  return !(fabsf(mean * rstd) < INFINITY);
+}
+
 // The same for the gradient, which loads two rows and keeps column sums.
 template <int TPR, int NV>
 struct NormBwdFlow {
@@ -319,7 +329,7 @@ struct NormBwdFlow {
   static constexpr int MIN_CTAS = TPR <= 32 ? 2 : (TPR == 128 ? 4 : 1);
 };
 
-template <bool VEC, int TPR, int NV, int XT, int GT>
+template <bool VEC, bool PADS, int TPR, int NV, int XT, int GT>
 __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN_CTAS)
     norm_bwd_kernel(const NormBwdParams p) {
   constexpr int E = XT == kRowBf16 && GT == kRowBf16 ? 8 : 4;
@@ -370,7 +380,7 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
       float sg = 0.f, sgx = 0.f;
 #pragma unroll
       for (int j = 0; j < EPT; ++j) {
-        // past the row's end d is 0, and with it every product
+        // past the row's end d is 0, and with it every product (see norm_pads_overflow)
         x[j] = (x[j] - mean[u]) * rstd[u];
         if (there) {
           aw[j] = fmaf(d[j], x[j], aw[j]);
@@ -379,6 +389,12 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
         d[j] *= w[j];
         sg += d[j];
         sgx = fmaf(d[j], x[j], sgx);
+      }
+      if (PADS && norm_pads_overflow(mean[u], rstd[u])) {
+        sgx = 0.f;
+#pragma unroll
+        for (int j = 0; j < EPT; ++j)
+          if (RowX::elem(lane, j) < p.dim) sgx = fmaf(d[j], x[j], sgx);
       }
       const float2 s = norm_sum2<TPR>(sg, sgx, slots, buf);
       const float mg = s.x * inv, mgx = s.y * inv;
@@ -441,7 +457,8 @@ __global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN
 // (2^-24) buries: of 200 K such rows the median was off by 6 %. Rows of three or
 // four values lose the digits where g happens to lie near the two directions (3 in
 // 1000 and 1 in 100000 off by more than 2e-5), rows of five no longer (none). fp64
-// costs nothing here: the time is the launch's and, for many rows, HBM's.
+// costs nothing here: 65536 fp32 rows of two take 5.0 us (12.4 with 16 threads a row
+// in fp32), one row 3.7 (3.1).
 constexpr int kNormFewDim = 4, kNormFewThreads = 256, kNormFewCtas = 2;
 
 __device__ __forceinline__ double norm_elem(const void* base, long long at, int bf16) {
@@ -653,7 +670,7 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, false)) norm_wide_ker
   }
 }
 
-template <int TPR, int NV>
+template <int TPR, int NV, bool PADS>
 __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, true))
     norm_bwd_wide_kernel(const NormBwdParams p, int stages) {
   constexpr int E = 4, EPT = 8 * NV;
@@ -710,13 +727,19 @@ __global__ void __launch_bounds__(TPR, norm_wide_ctas(TPR, true))
     if constexpr (!KEEP) norm_weights<true, TPR, NV, E>(p.w, 1.f, lane, p.dim, w);
 #pragma unroll
     for (int j = 0; j < EPT; ++j) {
-      // past the row's end d is 0, and with it every product
+      // past the row's end d is 0, and with it every product (see norm_pads_overflow)
       x[j] = (x[j] - mean) * rstd;
       aw[j] = fmaf(d[j], x[j], aw[j]);
       ab[j] += d[j];
       d[j] *= w[j];
       s[0] += d[j];
       s[1] = fmaf(d[j], x[j], s[1]);
+    }
+    if (PADS && norm_pads_overflow(mean, rstd)) {
+      s[1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < EPT; ++j)
+        if (Row::elem(lane, j) < p.dim) s[1] = fmaf(d[j], x[j], s[1]);
     }
     norm_sums<TPR, 2>(s, slots, buf);
     if ((lane & 31) == 0 && warp < 2 && ring.ok) copy_in(r + stages * step, ring.st, warp);

@@ -53,3 +53,23 @@ def test_layernorm_gradient_of_rows_of_a_few_values(dim, rows, xt, gt, dt):
         a = dy.clone()
         dsa.dsa_layernorm_bwd(a, x, None, mean, rstd, a)                               # in place
         assert torch.equal(a, dx)
+
+
+@pytest.mark.parametrize("dim", [5, 37, 129, 200, 1000, 1001, 1032, 2056, 4097, 9000])
+def test_layernorm_gradient_of_large_constant_rows(dim):
+    """Equal values of 1e36: hat is 0, but mean * rstd is past fp32, so places
+    past the row's end must not form it."""
+    g = _gen(dim)
+    rows = 7
+    x = torch.full((rows, dim), 1e36, device=DEV)
+    dy, w = _randn(g, rows, dim), _randn(g, dim)
+    mean, rstd = x[:, 0].clone(), torch.full((rows,), 1000.0, device=DEV)      # eps = 1e-6
+    n = dsa.layernorm_bwd_workspace(rows, dim)
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    dx, dw, db = torch.empty_like(x), torch.empty(dim, device=DEV), torch.empty(dim, device=DEV)
+    dsa.dsa_layernorm_bwd(dy, x, w, mean, rstd, dx, dw, db, ws, n)
+    q = dy.double() * w.double()
+    want = 1000.0 * (q - q.mean(-1, keepdim=True))
+    _within(dx, want, 1000.0 * (q.abs() + q.abs().mean(-1, keepdim=True)) * 73 * U, "dx")
+    assert (dw == 0).all()
+    _within(db, dy.double().sum(0), dy.double().abs().sum(0) * 64 * U, "dbias")
