@@ -666,7 +666,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (m_used == -INFINITY) {
 #pragma unroll
           for (int j = 0; j < 16; ++j) pk[j] = 0u;
-          lsum = lsum_mma = hmax != hmax ? hmax : 0.f;    // all -inf, or NaN among them
+          // no finite maximum so far: all visible logits are -inf, or NaN is among
+          // them (fmaxf leaves it out beside -inf, a masked key's among them)
+          bool nan = false;
+#pragma unroll
+          for (int j = 0; j < 32; ++j) nan |= z[j] != z[j];
+          lsum = lsum_mma = nan ? __int_as_float(0x7fffffff) : 0.f;
         }
         l += lsum;
         l_mma += lsum_mma;

@@ -73,3 +73,57 @@ def test_layernorm_gradient_of_large_constant_rows(dim):
     _within(dx, want, 1000.0 * (q.abs() + q.abs().mean(-1, keepdim=True)) * 73 * U, "dx")
     assert (dw == 0).all()
     _within(db, dy.double().sum(0), dy.double().abs().sum(0) * 64 * U, "dbias")
+
+
+# ------------------------------------------------------------------ dense attention
+
+@pytest.mark.parametrize("n", [1, 5, 31, 32, 33, 63, 64, 127, 128, 129, 160, 1153, 9473])
+def test_dense_nan_query(n):
+    """Every key's logit is NaN, whole rows and cut ones: out and lse are NaN, and
+    the heads beside it are as without it."""
+    c = _dense_case([n, 200], 1, 16, 128, n)
+    want, wlse = _dense(c)
+    for dim in (3, 570):
+        q = c["q"].clone()
+        q[0, 0, 2, dim] = math.nan
+        out, lse = _dense({**c, "q": q}, torch.float32)
+        assert out[0, 0, 2].isnan().all() and lse[0, 0, 2].isnan()
+        rest = [h for h in range(16) if h != 2]
+        assert torch.equal(out[0, 0, rest].bfloat16(), want[0, 0, rest]) and torch.equal(lse[0, 0, rest], wlse[0, 0, rest])
+        assert torch.equal(out[1].bfloat16(), want[1]) and torch.equal(lse[1], wlse[1])
+    dsa.dsa_check()
+
+
+@pytest.mark.parametrize("n", [1, 2, 33, 100, 129, 130, 1153, 9473])
+@pytest.mark.parametrize("dim", [0, 570])
+def test_dense_nan_in_one_key(n, dim):
+    """A visible key with NaN, in its value dims or only in its rotated ones, makes
+    its row NaN wherever it lies and the row is cut; behind the row it changes nothing."""
+    c = _dense_case([n, 77], 1, 40, 128, n + 1, room=n + 130)
+    want = _dense(c)
+    for at in sorted({0, n // 2, n - 1}):
+        kv = c["kv"].clone()
+        kv[c["rows"][0, at], dim] = math.nan
+        out, lse = _dense({**c, "kv": kv})
+        assert out[0].isnan().all() and lse[0].isnan().all(), at
+        assert torch.equal(out[1], want[0][1]) and torch.equal(lse[1], want[1][1])
+
+
+@pytest.mark.parametrize("n", [1, 20, 40, 300, 5000])
+def test_dense_logits_of_minus_infinity(n):
+    """Keys at minus infinity have no weight; NaN beside them still shows."""
+    c = _dense_case([n], 1, 8, 128, n + 2)
+    kv, q = c["kv"].clone(), c["q"].clone()
+    q[..., 575] = 1.0
+    kv[c["rows"][0, :n], 575] = -math.inf
+    out, lse = _dense({**c, "kv": kv, "q": q})
+    assert (out == 0).all() and (lse == -math.inf).all()             # as a row that sees no key
+    kv[c["rows"][0, n - 1], 574] = math.nan
+    out, lse = _dense({**c, "kv": kv, "q": q})
+    assert out.isnan().all() and lse.isnan().all()
+    if n > 1:                                                        # only the first key counts
+        kv = c["kv"].clone()
+        kv[c["rows"][0, 1:n], 575] = -math.inf
+        out, lse = _dense({**c, "kv": kv, "q": q}, torch.float32)
+        one = {**c, "kv": kv, "q": q}
+        _check_dense(one, out, lse, [[1]])
