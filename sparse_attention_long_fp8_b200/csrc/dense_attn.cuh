@@ -50,6 +50,7 @@
 // rows that see no key; 4-11 run the softmax and the epilogue.
 #pragma once
 
+#include "dense_loads.cuh"
 #include "layout.cuh"
 #include "ptx.cuh"
 
@@ -59,6 +60,7 @@ namespace dsa {
 
 constexpr int kDenseRowCost = 3;               // blocks
 constexpr int kDenseCutCost = 5;               // units
+constexpr unsigned long long kDenseDrainNs = 100'000'000ull;   // for a copy in flight, after a wait has run out
 constexpr int kDenseMinShare = 1;              // units (one row of 4000 keys: 14.8 us, 18.4 with 4)
 
 struct DenseParams {
@@ -374,17 +376,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
     // one phase meanwhile. `empty` has a barrier for the even and one for the odd
     // uses of a slot, so a wait for use u - 1 could be mistaken only for use u - 5,
     // 24 entries and more before, while a loader's entries are at most 11 apart.
-    const bool for_s = warp == 0;
+    // One elected lane makes the S loads. The V loads take the whole warp, which also
+    // zeroes the ends of partly filled entries: each of its waits is voted on, as a lane
+    // whose wait ran out while the others' just did not would leave the loop, and the
+    // warp's barriers, by itself. (Votes in both: 480 to 500 us for 64 sequences of
+    // 16-32 K keys, none in either 530 to 610, one lane for both 475; this 448.)
+    const bool for_s = warp == 0, lead = elect_one();
     uint32_t e0 = 0, segs = 0, tails = 0;        // e0: the segment's first entry
-    uint32_t mine = 0, phase = 0;                // slots this warp has filled, and their phases
+    DenseLoads<T::RING> loads;
     bool ok = true;
     DenseSeg w;
-    // The slot of entry e, once its last use has been read.
-    auto claim = [&](uint32_t e) -> uint32_t {
-      const uint32_t st = e % T::RING, u = e / T::RING;
-      if (u > 0) ok = mbar_wait(&empty[2 * st + ((u - 1) & 1)], ((u - 1) >> 1) & 1);
-      mine |= 1u << st;
-      phase = (phase & ~(1u << st)) | ((u & 1) << st);
+    auto voted = [&](uint64_t* bar, uint32_t parity) {
+      return __all_sync(0xffffffffu, mbar_wait(bar, parity)) != 0;
+    };
+    // The slot of entry e, once its last use has been read by `wait`; not ok:
+    // nothing is issued.
+    auto claim = [&](uint32_t e, auto wait) -> uint32_t {
+      uint32_t st;
+      ok = loads.claim(e, st, [&](uint32_t slot, uint32_t use) {
+        return wait(&empty[2 * slot + (use & 1)], (use >> 1) & 1);
+      });
       return st;
     };
     while (ok && walk.next(p, w)) {
@@ -397,27 +408,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
       };
       int y = locate(w.blk);
       if (for_s) {
-        // Q of this CTA's heads, once the previous segment's last S has read it
-        if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1);
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(q_full, T::QB * T::BOX);
-          tma_load_4d(q_smem, &tmap_q, q_full, 0, static_cast<int>(rank) * T::HB, 0, w.row);
-        }
-        ++segs;
-        for (int i = 0; i < w.n && ok; ++i) {
-          // S(i): this CTA's 64 keys, dims 128 t .. + 127 (the last entry: 64)
-          const uint32_t e = e0 + (i == 0 ? 0 : T::SE + (i - 1) * (T::SE + T::VE));
-          for (int t = 0; t < T::SE; ++t) {
-            const uint32_t st = claim(e + t);
-            if (!ok) break;
-            if (lane == 0) {
+        if (lead) {
+          // Q of this CTA's heads, once the previous segment's last S has read it
+          if (segs > 0) ok = mbar_wait(q_empty, (segs - 1) & 1);
+          if (ok) {
+            mbar_arrive_expect_tx(q_full, T::QB * T::BOX);
+            tma_load_4d(q_smem, &tmap_q, q_full, 0, static_cast<int>(rank) * T::HB, 0, w.row);
+            ++segs;
+          }
+          for (int i = 0; i < w.n && ok; ++i) {
+            // S(i): this CTA's 64 keys, dims 128 t .. + 127 (the last entry: 64)
+            const uint32_t e = e0 + (i == 0 ? 0 : T::SE + (i - 1) * (T::SE + T::VE));
+            for (int t = 0; t < T::SE; ++t) {
+              const uint32_t st = claim(e + t, mbar_wait);
+              if (!ok) break;
               mbar_arrive_expect_tx(&full[st], T::ENTRY);
               tma_load_3d(ring + st * T::ENTRY, &tmap_kv, &full[st], 0, y + static_cast<int>(rank) * 64, 2 * t);
             }
+            if (i + 1 < w.n) y = locate(w.blk + i + 1);
           }
-          if (i + 1 < w.n) y = locate(w.blk + i + 1);
         }
+        ok = __all_sync(0xffffffffu, ok);        // the other lanes' is true
       } else {
         for (int i = 0; i < w.n && ok; ++i) {
           // V(i): entry (key half kh, accumulator j): dims 256 j + 128 rank .. + 127
@@ -425,24 +436,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
           const uint32_t e = e0 + (i + 1 < w.n ? T::SE + i * (T::SE + T::VE) + T::SE
                                                : w.n * (T::SE + T::VE) - T::VE);
           for (int t = 0; t < T::VE; ++t) {
-            const uint32_t st = claim(e + t);
+            const uint32_t st = claim(e + t, voted);
             if (!ok) break;
             const int kh = t >> 1, zb = 4 * (t & 1) + 2 * static_cast<int>(rank);
             const int rows = valid - 64 * kh;    // of this half that hold keys
             uint8_t* dst = ring + st * T::ENTRY;
             if (rows >= 64 || rows <= 0) {
               // a half without keys reads as zeros: past the end of the pool
-              if (lane == 0) {
+              if (lead) {
                 mbar_arrive_expect_tx(&full[st], T::ENTRY);
                 tma_load_3d(dst, &tmap_kv, &full[st], 0,
                             rows > 0 ? y + 64 * kh : static_cast<int>(p.km.pool_rows), zb);
               }
             } else {
-              if (lane == 0) {
+              loads.by_tail(st);
+              if (lead) {
                 mbar_arrive_expect_tx(tail, T::ENTRY);
                 tma_load_3d(dst, &tmap_kv, tail, 0, y + 64 * kh, zb);
               }
-              ok = mbar_wait(tail, tails & 1) || mbar_wait(tail, tails & 1);
+              ok = voted(tail, tails & 1);
+              if (!ok) break;
+              loads.tail_landed();
               ++tails;
               for (int k = lane; k < (64 - rows) * 8; k += 32) {
                 sts_v4(smem_u32(dst) + rows * 128 + k * 16, 0u, 0u, 0u, 0u);
@@ -450,21 +464,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
               }
               fence_proxy_async_smem();
               __syncwarp();
-              if (lane == 0) mbar_arrive(&full[st]);
+              if (lead) mbar_arrive(&full[st]);
             }
           }
           if (i + 1 < w.n) y = locate(w.blk + i + 1);
         }
       }
       e0 += static_cast<uint32_t>(w.n) * (T::SE + T::VE);
-      __syncwarp();
     }
-    // A wait that ran out leaves copies in flight: they end before the CTA does.
-    if (!ok) {
-      for (uint32_t st = 0; st < T::RING; ++st)
-        if ((mine >> st) & 1u) mbar_wait(&full[st], (phase >> st) & 1u);
-      if (for_s && segs > 0) mbar_wait(q_full, (segs - 1) & 1);
+    // A wait that ran out leaves copies in flight: they end before the CTA does. (A
+    // slot that the other loader has used since has nothing of this one's in flight,
+    // and may count a phase more: its wait runs out after kDenseDrainNs.)
+    if (!ok && lead) {
+      loads.drain([&](uint32_t st, uint32_t ph) { mbar_wait_limit(&full[st], ph, kDenseDrainNs); },
+                  [&] { mbar_wait_limit(tail, tails & 1, kDenseDrainNs); });
+      if (for_s && segs > 0) mbar_wait_limit(q_full, (segs - 1) & 1, kDenseDrainNs);
     }
+    __syncwarp();
   } else if (warp == 1 && rank == 1) {
     // ------------------------------------------------------------ arrivals passed on to CTA 0
     if (elect_one()) {
@@ -636,8 +652,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(384, 1)
         if (i > 0 && __any_sync(0xffffffffu, grow)) {
           tc_fence_after();
           const float alpha = grow ? ex2_approx(m_used - m_new) : 1.0f;
+          const bool all_ok = __all_sync(0xffffffffu, ok);       // the loads take whole warps
 #pragma unroll 1
-          for (int c = half * 128; c < (half + 1) * 128 && ok; c += 16) {
+          for (int c = half * 128; c < (half + 1) * 128 && all_ok; c += 16) {
             uint32_t o[16];
             tmem_ld16(tmem_base + lane_addr + T::COL_O + c, o);
             tmem_wait_ld();
