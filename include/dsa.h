@@ -160,7 +160,8 @@ dsa_status dsa_indexer_scores_ex(const dsa_shape* shape, const dsa_layout* layou
  * values: scale[r] = amax_r / 448 (1 when the row is all zero), and
  * codes[r, d] = E4M3(clamp(x[r, d] / scale[r], -448, 448)) rounded to
  * nearest even (saturating, sign of zero kept). scale and x / scale are
- * fp32 IEEE operations, so the codes are reproducible bit for bit.
+ * fp32 IEEE operations, so the codes are reproducible bit for bit. x is taken
+ * to be finite: NaN is not looked for, and takes the code of -448.
  *   x      [rows, dim] bf16 (raw bits)   (2 * dim / 32 -byte aligned)
  *   codes  [rows, dim] e4m3fn codes      (dim / 32 -byte aligned)
  *   scales [rows] fp32
@@ -475,7 +476,13 @@ dsa_status dsa_layernorm_bwd(int64_t rows, int32_t dim, const void* dy, int32_t 
  *           past n_new[b] are padding and write nothing
  *   k_fp8, k_scale, kv: the caches (layout as for dsa_forward; NULL =
  *           contiguous [B, n_kv, ...]). n_kv of the shape is their capacity.
- *   The key stays in fp32 from its load to its codes. A token whose position
+ *   The key stays in fp32 from its load to its codes. It is divided by its scale
+ *   through the scale's reciprocal, so where the quotient lies within 2^-22 of a
+ *   border between two codes it may take the other one than
+ *   dsa_quantize_e4m3's division would. NaN in the encoded key stays: NaN codes
+ *   at its dims and scale 1 (a key with NaN or infinity in k is NaN throughout,
+ *   by its norm); infinity gives scale infinity, NaN codes at its dims and zeros
+ *   elsewhere. A token whose position
  *   is outside [0, n_kv), or whose page is outside the pool, writes nothing
  *   and the next dsa_check() returns DSA_ERR_INVALID_ARG. Two sequences must
  *   not append to one page; layout->row_pos must be NULL (a sequence's new

@@ -175,19 +175,20 @@ __device__ __forceinline__ void append_token(const AppendParams& p, uint32_t tok
       v[j] = second ? o * t.y + v[j] * t.x : v[j] * t.x - o * t.y;
     }
   }
-  float amax = 0.f;
+  // the sizes as bit patterns: non-negative floats order like these, and NaN is above all
+  uint32_t top = 0;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) amax = fmaxf(amax, fabsf(v[j]));
-  // non-negative floats order like their bit patterns
-  amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
-  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;
+  for (int j = 0; j < PER; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+  const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, top));
+  const float scale = amax > 0.f ? __fdiv_rn(amax, 448.f) : 1.f;     // 1 with NaN
   // v / scale to 2^-23 by one reciprocal, unless that would overflow
   const bool tiny = scale < 1e-37f;
   const float inv = __frcp_rn(tiny ? 1.f : scale);
   uint32_t packed = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
-    const float y = fminf(448.f, fmaxf(-448.f, tiny ? __fdiv_rn(v[j], scale) : v[j] * inv));
+    // saturates at 448, which is in reach by a rounding only; NaN stays NaN
+    const float y = tiny ? __fdiv_rn(v[j], scale) : v[j] * inv;
     packed |= static_cast<uint32_t>(__nv_cvt_float_to_fp8(y, __NV_SATFINITE, __NV_E4M3)) << (8 * j);
   }
   uint8_t* codes = p.k_fp8 + at * DI + lane * PER;

@@ -127,3 +127,87 @@ def test_dense_logits_of_minus_infinity(n):
         out, lse = _dense({**c, "kv": kv, "q": q}, torch.float32)
         one = {**c, "kv": kv, "q": q}
         _check_dense(one, out, lse, [[1]])
+
+
+# ------------------------------------------------------------------ cache append
+
+def _append(k, w, b, rk, idx, page=128):
+    """One token per sequence at position 5 of fresh caches: codes (as values),
+    scales, latent rows, in the sequences' order."""
+    B = k.shape[0]
+    ca = _cache(B, 256, page, idx, 64, 3)
+    shape = dsa.DsaShape(B, 1, 256, 64, idx, 2048, 128, 64, 64, 1.0)
+    c = torch.ones(B, 1, 64, device=DEV, dtype=torch.bfloat16)
+    dsa.dsa_cache_append(shape, k, w, b, 1e-6, rk, c, dsa.rope_spec(8), torch.full((B,), 5, dtype=torch.int32, device=DEV),
+                         None, ca["codes"], ca["scale"], ca["kv"], layout=ca["layout"])
+    dsa.dsa_check()
+    at = ca["rows"][:, 5]
+    return ca["codes"][at].view(torch.float8_e4m3fn).float(), ca["scale"][at], ca["kv"][at]
+
+
+@pytest.mark.parametrize("idx", [32, 128])
+@pytest.mark.parametrize("layout", [dsa.DSA_ROPE_HALF, dsa.DSA_ROPE_INTERLEAVED])
+@pytest.mark.parametrize("rot,begin", [(8, 0), (8, 16), (6, 3)])
+def test_append_keys_that_are_not_finite(rot, begin, layout, idx):
+    g = _gen(idx + rot)
+    B, rk = 6, dsa.rope_spec(rot, rot_begin=begin, layout=layout)
+    k = _randn(g, B, 1, idx, dtype=torch.bfloat16)
+    want = _append(k, None, None, rk, idx)
+    assert want[0].isfinite().all()
+    bad = k.clone()
+    bad[0, 0, 0] = bad[1, 0, idx - 1] = bad[2, 0, begin] = math.nan
+    bad[3, 0, 7], bad[4, 0, idx // 2] = math.inf, -math.inf
+    codes, scale, kv = _append(bad, None, None, rk, idx)
+    # the norm spreads NaN and infinity over the whole key: NaN codes, scale 1
+    assert codes[:5].isnan().all() and (scale[:5] == 1.0).all()
+    assert torch.equal(codes[5], want[0][5]) and scale[5] == want[1][5] and torch.equal(kv, want[2])
+    # a bias that is not finite: only its own dim, outside the rotated part, is
+    b = torch.zeros(idx, device=DEV)
+    b[idx - 2] = math.nan
+    rest = [i for i in range(idx) if i != idx - 2]
+    codes, scale, _ = _append(k, None, b, rk, idx)
+    assert codes[:, idx - 2].isnan().all() and (scale == 1.0).all()
+    # the other values against scale 1: half a step of e4m3, 2^-4 of the value, 2^-10 below 2^-6
+    was = (want[0] * want[1][:, None])[:, rest]
+    step = torch.maximum(was.abs() * 2.0 ** -4, torch.full_like(was, 2.0 ** -10))
+    # `was` itself is off by half a step of its own code
+    own = torch.maximum(was.abs() * 2.0 ** -4, want[1][:, None] * 2.0 ** -10)
+    assert ((codes[:, rest] - was).abs() <= (step + own) * 1.07).all()
+    b[idx - 2] = math.inf
+    codes, scale, _ = _append(k, None, b, rk, idx)
+    assert (scale == math.inf).all() and codes[:, idx - 2].isnan().all() and (codes[:, rest] == 0).all()
+
+
+def test_append_nan_key_leaves_the_other_keys_scores_and_choices():
+    g = _gen(77)
+    n, topk = 300, 64
+    shape = dsa.DsaShape(1, n, n, 64, 128, topk, 128, 576, 512, 1.0 / 24)
+    one = dsa.DsaShape(1, 1, n, 64, 128, topk, 128, 576, 512, 1.0 / 24)
+    rk, rc = dsa.rope_spec(64), dsa.rope_spec(64, rot_begin=512)
+    k, c = _randn(g, 1, n, 128, dtype=torch.bfloat16), _randn(g, 1, n, 576, dtype=torch.bfloat16)
+    iq, w = _randn(g, 1, 1, 64, 128, dtype=torch.bfloat16), _randn(g, 1, 1, 64).abs()
+    qc, qs = torch.empty(1, 1, 64, 128, dtype=torch.uint8, device=DEV), torch.empty(1, 1, 64, device=DEV)
+    dsa.dsa_quantize_e4m3(iq, qc, qs)
+    pos, lens = torch.tensor([n - 1], dtype=torch.int32, device=DEV), torch.tensor([n], dtype=torch.int32, device=DEV)
+    got = []
+    for bad in (False, True):
+        kk = k.clone()
+        if bad:
+            kk[0, 17, 3] = math.nan
+        ca = _cache(1, n, 128, 128, 576, 9)
+        dsa.dsa_cache_append(shape, kk, None, None, 1e-6, rk, c, rc, None, None, ca["codes"], ca["scale"], ca["kv"],
+                             layout=ca["layout"])
+        scores = torch.empty(1, 1, n, device=DEV)
+        dsa.dsa_indexer_scores(one, qc, qs, w, ca["codes"], ca["scale"], pos, lens, 0, 1, scores, layout=ca["layout"])
+        idx = torch.empty(1, 1, topk, dtype=torch.int32, device=DEV)
+        dsa.dsa_indexer_topk(one, qc, qs, w, ca["codes"], ca["scale"], pos, lens, 0, 1, idx, layout=ca["layout"])
+        dsa.dsa_check()
+        got.append((scores.view(-1), idx.view(-1).tolist()))
+    rest = [i for i in range(n) if i != 17]
+    assert torch.equal(got[0][0][rest], got[1][0][rest])
+    for s, idx in got:
+        chosen = [i for i in idx if i != 17]
+        assert len(set(idx)) == topk and min(idx) >= 0 and max(idx) < n
+        # all but key 17 in the order of their scores
+        kth = s[rest].sort(descending=True).values[len(chosen) - 1]
+        assert (s[chosen] >= kth).all()
