@@ -395,7 +395,9 @@ typedef struct {
  *   DSA_ROPE_YARN    (1 - g) f_i / factor + g f_i, with
  *                    g = clamp((r - beta_slow) / (beta_fast - beta_slow), 0, 1)
  *                    and r = orig_context f_i / (2 pi), the turns that pair i
- *                    makes over the original context.
+ *                    makes over the original context. DeepSeek's released
+ *                    code ramps over the pair's index between rounded bounds
+ *                    instead: for its checkpoints write those f_i to freq.
  * factor, orig_context and the betas are looked at only where they are used.
  * Host-only.
  */
@@ -421,7 +423,8 @@ typedef struct {
  *   otherwise the other dims are copied, and out must not overlap x.
  *   A token at a negative position is padding: its rows of out are left as
  *   they were.
- *   Arithmetic in fp32 with angles reduced in fp64; one rounding to dtype.
+ *   Arithmetic in fp32 with angles reduced in fp64 (cos and sin are off by
+ *   2^-23 and by 2^-52 of the whole angle in radians); one rounding to dtype.
  */
 dsa_status dsa_rope(const dsa_rope_spec* spec, const dsa_rope_view* view, const void* x, void* out,
                     const int32_t* q_pos0, const int32_t* row_pos, int32_t backward, void* stream);

@@ -6,8 +6,10 @@
 // (interleaved).
 //
 // The angle is formed in turns, pos * (freq / 2 pi), in fp64 and reduced there to
-// an eighth of a turn, which goes on in fp32: at position 2^20 an fp32 product
-// would be off by 2^-4 radians, the reduced angle is off by 2^-25 at any position.
+// an eighth of a turn, which goes on in fp32. An fp32 product would be off by 2^-4
+// radians at position 2^20. The reduced angle is off by 2^-25 for its rounding to
+// fp32, and by 2^-52 of the whole angle for the roundings of freq / 2 pi and of the
+// product: as much again at 2^27 radians, 2^-21 at the last position (freq = 1).
 // Every (token, pair) is evaluated once per CTA, into shared memory, and used by
 // all heads of the CTA's rows.
 //
@@ -58,7 +60,7 @@ struct RopeAngles {
 // 1/8, x = 2 pi rest in [-pi/4, pi/4], in fp64 up to the one rounding of x; sin x
 // and cos x by their Taylor series (the first terms left out are below
 // x^11 / 11! = 2e-9 and x^12 / 12! = 2e-10), turned by q quarters. Off by about an
-// ulp. (With the fraction itself rounded to fp32 the angle is off by up to 1e-7: of
+// ulp of 1, and by the angle's own error far out (see the top). (With the fraction itself rounded to fp32 the angle is off by up to 1e-7: of
 // 80 M appended E4M3 codes 148 instead of 121 miss the 64-bit formula's; a form with
 // cos and sin rounded from 64 bits misses 128.)
 __device__ __forceinline__ float2 rope_cos_sin(double turns, int pos, float amplitude) {

@@ -2,6 +2,8 @@
 that are not finite, positions far out. Tolerances count roundings as in
 test_gpu_next.py."""
 import math
+import random
+from fractions import Fraction
 
 import pytest
 import torch
@@ -211,3 +213,37 @@ def test_append_nan_key_leaves_the_other_keys_scores_and_choices():
         # all but key 17 in the order of their scores
         kth = s[rest].sort(descending=True).values[len(chosen) - 1]
         assert (s[chosen] >= kth).all()
+
+
+# ------------------------------------------------------------------ rotary positions
+
+# 2 pi to 60 digits
+_TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
+
+
+@pytest.mark.parametrize("layout", [dsa.DSA_ROPE_HALF, dsa.DSA_ROPE_INTERLEAVED])
+@pytest.mark.parametrize("back", [False, True])
+def test_rope_cos_and_sin_to_an_ulp(layout, back):
+    """Pairs (1, 0) turn to (cos, sin) exactly as the kernel forms them, against
+    the exact product of position and frequency, reduced exactly."""
+    spec = dsa.rope_spec(16, layout=layout)
+    rnd = random.Random(5)
+    pos = [0, 1, 2, 3, 1000, 65535, 1 << 20, (1 << 27) - 1, (1 << 29) + 7, (1 << 31) - 2]
+    pos += [int(2.0 ** rnd.uniform(0, 31)) for _ in range(500)]
+    freq = [Fraction(spec.freq[i]) for i in range(8)]
+    angle = [[(p * f) - _TWO_PI * round(p * f / _TWO_PI) for f in freq] for p in pos]
+    want = torch.tensor([[[math.cos(a), (-1 if back else 1) * math.sin(a)] for a in map(float, r)] for r in angle],
+                        dtype=torch.float64, device=DEV)
+    x = torch.zeros(1, len(pos), 1, 16, device=DEV)
+    first = slice(0, 8) if layout == dsa.DSA_ROPE_HALF else slice(0, 16, 2)
+    second = slice(8, 16) if layout == dsa.DSA_ROPE_HALF else slice(1, 16, 2)
+    x[..., first] = 1.0
+    y = torch.empty_like(x)
+    dsa.dsa_rope(spec, x, y, row_pos=torch.tensor([pos], dtype=torch.int32, device=DEV), backward=back)
+    got = torch.stack([y[0, :, 0, first], y[0, :, 0, second]], -1)
+    # the rest of the angle rounds by half an ulp below 1: 2^-25 = U / 2. sin: its last
+    # fma U / 2 (values below 1), the cube's and the series' roundings 4 U of at most
+    # 0.617 / 6 of the value: U / 2. cos: its last fma U / 2, the square's U of 0.31, the
+    # series' 3 U of 0.31: 1.3 U. Left out of the series: U / 28.
+    whole = torch.tensor([[float(p * f) for f in freq] for p in pos], dtype=torch.float64, device=DEV)
+    _within(got, want, (2.4 * U + whole * 2.0 ** -52)[..., None], "cos, sin")
