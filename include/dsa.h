@@ -349,7 +349,9 @@ dsa_status dsa_indexer_kl(const dsa_shape* shape, const uint8_t* q_fp8,
  *   p = softmax(softmax_scale * q . kv[s]) over every key s the row sees
  *   (s <= position and s < kv_len), out = p kv[:, :D_v].
  *   A row that sees no key gets out = 0 and lse = -inf. Cache rows past
- *   kv_len are never used, whatever they hold. p is rounded to bf16 for the
+ *   kv_len are never used, whatever they hold. Keys on a page outside the pool
+ *   count as rows of zeros, with logit 0 (see dsa_layout): the row's out and
+ *   lse are then not those of its other keys alone. NaN among the logits a row sees makes its out and lse NaN. p is rounded to bf16 for the
  *   product with V and O is divided by the sum of the rounded p; every sum,
  *   maximum and the lse are fp32.
  *   The caches' keys are cut into equal shares per SM pair on the device, so

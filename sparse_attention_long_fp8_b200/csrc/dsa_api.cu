@@ -1917,7 +1917,7 @@ dsa_status dsa_check(void* stream) {
     if (word & dsa::kErrBadInput)
       return fail(DSA_ERR_INVALID_ARG,
                   "a block-table page was outside the key pool, or an append past its cache; its "
-                  "keys were skipped (error word 0x%x)",
+                  "keys were neither read nor written (error word 0x%x)",
                   word);
     return fail(DSA_ERR_CUDA, "device error word 0x%x", word);
   }
