@@ -348,12 +348,13 @@ dsa_status dsa_indexer_kl(const dsa_shape* shape, const uint8_t* q_fp8,
  *   lse     [B, n_q, H] fp32 natural-log sum of exp of the logits, or NULL
  *   p = softmax(softmax_scale * q . kv[s]) over every key s the row sees
  *   (s <= position and s < kv_len), out = p kv[:, :D_v].
- *   A row that sees no key gets out = 0 and lse = -inf. Cache rows past
- *   kv_len are never used, whatever they hold. Keys on a page outside the pool
- *   count as rows of zeros, with logit 0 (see dsa_layout): the row's out and
- *   lse are then not those of its other keys alone. NaN among the logits a row sees makes its out and lse NaN. p is rounded to bf16 for the
- *   product with V and O is divided by the sum of the rounded p; every sum,
- *   maximum and the lse are fp32.
+ *   A row that sees no key gets out = 0 and lse = -inf; NaN among the logits
+ *   that a row sees makes its out and lse NaN. Cache rows past kv_len are never
+ *   used, whatever they hold. Keys on a page outside the pool count as rows of
+ *   zeros, with logit 0 (see dsa_layout): the row's out and lse are then not
+ *   those of its other keys alone. p is rounded to bf16 for the product with V
+ *   and O is divided by the sum of the rounded p; every sum, maximum and the
+ *   lse are fp32.
  *   The caches' keys are cut into equal shares per SM pair on the device, so
  *   lengths may be ragged; the results are the same bits on every call.
  *   Supported: qk_dim = 576, v_dim = 512, heads 1..128, softmax_scale > 0,
