@@ -788,11 +788,13 @@ dsa_status launch_dense(const dsa_shape* s, const HostLayout& lay, const uint16_
   p.H = s->heads;
   p.out_bf16 = out_bf16;
   p.pairs = pl.pairs;
-  // Rows that the kernel's own rule (keep_whole) would leave whole whatever the
-  // lengths, from a share's least size and the longest row that the caches can
-  // hold: no join is launched. With some rows the launch that this saves, 2 us,
-  // is worth a few blocks more (16 rows of 350 to 700 keys: 18.6 us, 20.5 with a
-  // join that finds nothing).
+  // The longest row that the caches can hold, put to the kernel's rule (keep_whole)
+  // with the least share. Where it says whole the lengths need not be asked, and no
+  // join is launched; up to one row per pair it may say so a few blocks later than
+  // the kernel's (a fifth of a unit per row in place of an eighth), as a join that
+  // finds nothing costs 2 us too. 64 rows in caches of 1920 keys, whole against
+  // asked: all full 43.4 us and 47.7; every other one a quarter full 38.0 and 42.8; one
+  // full, the others 128 keys: 32.8 and 24.5, what the host cannot see.
   const int most = (s->n_kv + 127) / 128 + dsa::kDenseRowCost;
   p.whole = p.rows <= p.pairs ? most <= dsa::kDenseMinShare + dsa::kDenseCutCost + p.rows / 5
                               : most / 2 <= dsa::kDenseCutCost + p.pairs / 8;
@@ -940,7 +942,7 @@ unsigned norm_grid(int64_t rows, int dim, bool gradient, bool wide) {
   } else {
     const int tpr = norm_pick(dim).tpr;
     groups = norm_groups(tpr);
-    per_sm = gradient ? (tpr <= 32 ? 2 : (tpr == 128 ? 4 : 1)) : (tpr <= 32 ? 4 : (tpr == 128 ? 6 : (tpr == 512 ? 2 : 1)));
+    per_sm = dsa::norm_ctas(tpr, gradient);
   }
   const int64_t most = static_cast<int64_t>(num_sms()) * per_sm;
   return static_cast<unsigned>(std::max<int64_t>(1, std::min((rows + groups - 1) / groups, most)));

@@ -225,19 +225,22 @@ __device__ __forceinline__ float norm_sum(float a, float2* slots, int& buf) {
 template <int TPR>
 constexpr int norm_threads() { return TPR <= 32 ? 256 : TPR; }
 
+// CTAs per SM that the registers are bounded for, without and with the gradient.
+constexpr int norm_ctas(int tpr, bool gradient) {
+  return gradient ? (tpr <= 32 ? 2 : tpr == 128 ? 4 : 1) : (tpr <= 32 ? 4 : tpr == 128 ? 6 : tpr == 512 ? 2 : 1);
+}
+
 // How a group keeps bytes in flight: narrow rows are loaded U at a time, wide
-// ones one row ahead (PRE), the others rely on the other CTAs. MIN_CTAS per SM
-// bounds the registers.
+// ones one row ahead (PRE), the others rely on the other CTAs.
 template <int TPR, int NV, int TYPE>
 struct NormFlow {
   static constexpr int U = TPR <= 32 && NV == 1 ? (TYPE == kRowBf16 ? 4 : 2) : 1;
   static constexpr bool PRE = U == 1 && NV == 1;
   static constexpr bool KEEP = NV == 1;                  // weights stay in registers
-  static constexpr int MIN_CTAS = TPR <= 32 ? 4 : (TPR == 128 ? 6 : (TPR == 512 ? 2 : 1));
 };
 
 template <bool VEC, int TPR, int NV, int TYPE>
-__global__ void __launch_bounds__(norm_threads<TPR>(), NormFlow<TPR, NV, TYPE>::MIN_CTAS)
+__global__ void __launch_bounds__(norm_threads<TPR>(), norm_ctas(TPR, false))
     norm_kernel(const NormParams p) {
   constexpr int E = TYPE == kRowBf16 ? 8 : 4;
   using Row = NormRow<VEC, TPR, NV, TYPE, E>;
@@ -326,11 +329,10 @@ struct NormBwdFlow {
   static constexpr int U = TPR <= 32 && NV == 1 ? 2 : 1;
   static constexpr bool PRE = U == 1 && NV == 1;
   static constexpr bool KEEP = NV == 1;
-  static constexpr int MIN_CTAS = TPR <= 32 ? 2 : (TPR == 128 ? 4 : 1);
 };
 
 template <bool VEC, bool PADS, int TPR, int NV, int XT, int GT>
-__global__ void __launch_bounds__(norm_threads<TPR>(), NormBwdFlow<TPR, NV>::MIN_CTAS)
+__global__ void __launch_bounds__(norm_threads<TPR>(), norm_ctas(TPR, true))
     norm_bwd_kernel(const NormBwdParams p) {
   constexpr int E = XT == kRowBf16 && GT == kRowBf16 ? 8 : 4;
   using RowX = NormRow<VEC, TPR, NV, XT, E>;
