@@ -8,7 +8,7 @@
 // (the others are copied).
 //
 // A warp takes one token. Floor: HBM, 2 (d^I + D_qk) bytes read and d^I + 4 + 2
-// D_qk written per token. What bounds it is issuing, 440 instructions per token
+// D_qk written per token. What bounds it is issuing, 445 instructions per token
 // and warp, in a chain of two loads, reductions and stores that 32 warps per SM
 // hide in part: 19.7 us for 26 K tokens, 3.55 TB/s (without the key's part or
 // without the latent row's it would be 14.9). Two tokens per warp, 16 lanes each:
